@@ -164,6 +164,13 @@ def _hadamard(dim, dtype):
 
 
 def prepare(case, seed):
+    st = _inputs(case, seed)
+    if own:
+        st["calls"], st["written"] = _bound(st)
+    return st
+
+
+def _inputs(case, seed):
     c, gen = case, torch.Generator(device=DEV)
     gen.manual_seed(seed)
     S = c["seqs"]
@@ -224,42 +231,34 @@ def prepare(case, seed):
 
 # ---------------------------------------------------------------- one pass
 def run(st):
-    op = st["case"]["op"]
     if own:
-        return _OWN[op](st)
-    return _PLAIN[op](st)
+        for call in st["calls"]:
+            call()
+        return st["written"]
+    return _PLAIN[st["case"]["op"]](st)
 
 
-def _own_map(st):
+def _bound(st):
+    """The prepared calls that a serving loop keeps beside its buffers, and what they write."""
     from kv_cache_rotation_b200 import torch_api as TA
+    c = st["case"]
+    if c["op"] == "prompt":
+        Hq, H, x = c["q_heads"], c["heads"], st["qkv"]
+        call = TA.bind_attend_prompt(x[:, :Hq], x[:, Hq:Hq + H], x[:, Hq + H:], st["cu"], st["max_rows"], st["scale"], st["out"])
+        return [call], st["out"]
     b = st["batch"]
-    TA.page_map(st["desc"], b, st["ctx"], st["new"], st["free"], st["used"], st["report"])
-    return dict(cu=b.cu_rows, kv_len=b.kv_len, table=b.block_table, seq=b.seq, pos=b.pos, slot=b.slot, report=st["report"])
-
-
-def _own_cache(st):
-    from kv_cache_rotation_b200 import torch_api as TA
-    H = st["case"]["heads"]
-    TA.encode_paged(st["dk"], st["kv"][:, :H], st["batch"], st["tk"], st["kc"])
-    TA.encode_paged(st["dv"], st["kv"][:, H:], st["batch"], st["tv"], st["vc"])
-    TA.decode_paged(st["dk"], st["kc"], st["batch"], st["tk"], st["back"][0])
-    TA.decode_paged(st["dv"], st["vc"], st["batch"], st["tv"], st["back"][1])
-    return dict(k=st["back"][0], v=st["back"][1])
-
-
-def _own_paged(st):
-    from kv_cache_rotation_b200 import torch_api as TA
-    TA.attend_paged(st["dk"], st["dv"], st["q"], st["kc"], st["tk"], st["vc"], st["tv"], st["batch"], st["max_rows"], st["max_kv"],
-                    st["scale"], st["out"], st["ws"])
-    return st["out"]
-
-
-def _own_prompt(st):
-    from kv_cache_rotation_b200 import torch_api as TA
-    Hq, H = st["case"]["q_heads"], st["case"]["heads"]
-    x = st["qkv"]
-    TA.attend_prompt(x[:, :Hq], x[:, Hq:Hq + H], x[:, Hq + H:], st["cu"], st["max_rows"], st["scale"], st["out"])
-    return st["out"]
+    if c["op"] == "map":
+        call = TA.bind_page_map(st["desc"], b, st["ctx"], st["new"], st["free"], st["used"], st["report"])
+        return [call], dict(cu=b.cu_rows, kv_len=b.kv_len, table=b.block_table, seq=b.seq, pos=b.pos, slot=b.slot, report=st["report"])
+    if c["op"] == "cache":
+        H, kv, (k, v) = c["heads"], st["kv"], st["back"]
+        return [TA.bind_encode_paged(st["dk"], kv[:, :H], b, st["tk"], st["kc"]),
+                TA.bind_encode_paged(st["dv"], kv[:, H:], b, st["tv"], st["vc"]),
+                TA.bind_decode_paged(st["dk"], st["kc"], b, st["tk"], k),
+                TA.bind_decode_paged(st["dv"], st["vc"], b, st["tv"], v)], dict(k=k, v=v)
+    call = TA.bind_attend_paged(st["dk"], st["dv"], st["q"], st["kc"], st["tk"], st["vc"], st["tv"], b, st["max_rows"], st["max_kv"],
+                                st["scale"], st["out"], st["ws"])
+    return [call], st["out"]
 
 
 # ---------------------------------------------------------------- plain forms
@@ -425,7 +424,6 @@ def _plain_prompt(st):
 
 
 _PLAIN = dict(map=_plain_map, cache=_plain_cache, paged=_plain_paged, prompt=_plain_prompt)
-_OWN = dict(map=_own_map, cache=_own_cache, paged=_own_paged, prompt=_own_prompt)
 
 
 # ---------------------------------------------------------------- what a pass cannot do without
@@ -454,7 +452,7 @@ def work(case):
 
 # ---------------------------------------------------------------- in 64 bits
 def exact(case, seed):
-    st = prepare(case, seed)
+    st = _inputs(case, seed)
     c = case
     if c["op"] == "map":
         return None
