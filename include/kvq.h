@@ -267,6 +267,111 @@ kvq_status kvq_attend_noalloc(const kvq_desc* dk, const kvq_desc* dv, const void
 /* Workspace bytes kvq_attend needs for these arguments; 0 if they are invalid or unsupported. */
 size_t kvq_attend_workspace_bytes(const kvq_desc* dk, const kvq_desc* dv, int32_t q_heads, int32_t n_tokens);
 
+/* ---- The paged cache: the same records in pages that sequences of different lengths share.
+ *
+ * A descriptor of a paged cache has batch = pages of the pool and t_cap = page size in tokens (any
+ * positive number), so codes and scale_zero are sized by kvq_packed_bytes and laid out as ever: slot
+ * o of page p is record (p*H + h)*t_cap + o. tokens, t0 and group_heads are ignored; rot is NONE or
+ * FWHT_HEAD and quant MINMAX (else KVQ_ERR_UNSUPPORTED). pages * page size must stay below 2^31.
+ * Sinks are the positions below n_sink (no list); their fp16 rows are kept by sequence, not by page:
+ * kvq_packed.sink is half [sink_rows][H][n_sink][head_dim], and sequence s owns row sink_slot[s]
+ * (row s where sink_slot is NULL).
+ *
+ * The rows of a call (new tokens) are packed on one axis: sequence s has the rows
+ * cu_rows[s] .. cu_rows[s+1]-1, in token order. All pointers are device pointers, int32; kvq_page_map
+ * fills them, or the caller does. Values that do not fit (a slot outside the pool, a page outside
+ * 0..batch-1, a position without a RoPE row) are never followed: the row or the key is left out. */
+typedef struct {
+  int32_t n_seqs;       /* S >= 0 sequences */
+  int32_t n_rows;       /* rows of the packed axis; rows behind cu_rows[S] belong to no sequence */
+  int32_t max_pages;    /* entries of a block_table row, > 0 */
+  int32_t sink_rows;    /* sequences the sink buffers hold (n_sink > 0) */
+  int32_t* cu_rows;     /* [S+1] ascending from 0 */
+  int32_t* kv_len;      /* [S] cached tokens, the call's new ones included */
+  int32_t* block_table; /* [S][max_pages] page of positions k*t_cap .. k*t_cap + t_cap-1 */
+  int32_t* seq;         /* [n_rows] sequence of a row, -1 for none; 16-byte aligned, like the next two */
+  int32_t* pos;         /* [n_rows] position of a row in its sequence */
+  int32_t* slot;        /* [n_rows] page * t_cap + offset of a row's record, -1 for none */
+  const int32_t* sink_slot; /* [S] or NULL */
+} kvq_paged;
+
+/* Block tables and slot maps from a batch's lengths, on the device: sequence s holds ctx_len[s] cached
+ * tokens and gets new_len[s] more (negative values count as 0). In order of s each sequence takes the
+ * pages it lacks, ceil((ctx+new)/t_cap) - ceil(ctx/t_cap), from free_pages[free_used[0] ..
+ * n_free-1], in order; they are written behind its present entries of block_table, which the call
+ * reads and does not change. Written: cu_rows, kv_len = ctx + new, the new block_table entries, and
+ * for every row seq, pos and slot (-1 in rows that belong to no sequence).
+ * report int32[4]: rows of all sequences; free pages taken in all, earlier calls' included (the next
+ * call's free_used); rows without a slot because the pool or a block_table row ran out (their pages
+ * read -1); pages that were lacking. report must not overlap free_used.
+ * Of pg n_seqs, n_rows, max_pages and the six arrays are used; of d batch and t_cap. n_seqs <= 16384
+ * (else KVQ_ERR_UNSUPPORTED). One launch; the result does not depend on scheduling. */
+kvq_status kvq_page_map(const kvq_desc* d, const kvq_paged* pg, const int32_t* ctx_len, const int32_t* new_len,
+                        const int32_t* free_pages, int32_t n_free, const int32_t* free_used, int32_t* report,
+                        kvq_stream_t stream);
+
+/* kvq_encode of packed rows into pages: row r of x, half [n_rows][H][head_dim] with x_stride elements
+ * between rows (a multiple of 8, at least H*head_dim; 16-byte aligned), goes to record slot[r], turned
+ * to position pos[r] when d->rope; the record is the one that kvq_encode gives. Sink positions (pos <
+ * n_sink) are also copied to the sequence's sink row. Rows without a slot are skipped. Slots given
+ * twice in one call end with either row's record. cu_rows, kv_len and block_table are not read. */
+kvq_status kvq_encode_paged(const kvq_desc* d, const void* x, int64_t x_stride, const kvq_paged* pg,
+                            const kvq_tables* tb, const kvq_packed* out, kvq_stream_t stream);
+
+/* kvq_decode of packed rows out of pages: row r of x_out (fp32 if out_fp32, else fp16; x_stride as
+ * above, in elements) gets the decoded record slot[r], or the sink row of a sink position. Rows
+ * without a slot are left as they were. */
+kvq_status kvq_decode_paged(const kvq_desc* d, const kvq_packed* in, const kvq_paged* pg, const kvq_tables* tb,
+                            void* x_out, int64_t x_stride, int32_t out_fp32, kvq_stream_t stream);
+
+/* Attention of each sequence's new rows over its pages of the compressed cache, causal: row i of
+ * the m rows of sequence s is at position p = kv_len[s] - m + i and
+ *   out[r][qh] = sum_{n <= p} softmax_n(scale * <q[r][qh], khat_n>) vhat_n
+ * with khat and vhat as for kvq_attend (the call's own tokens are read from the cache: encode them
+ * first). One row per sequence is a decode step; more are a chunk of a prompt. Keys whose page is
+ * missing from block_table are left out; a row that sees no key gets zeros; rows behind cu_rows[S]
+ * are left as they were.
+ *   q, out   half [n_rows][q_heads][head_dim], q_stride / out_stride elements between rows (multiples
+ *            of 8), 16-byte aligned, q RoPE'd at its positions; q_heads a multiple of H, at most 128*H
+ *   dk, dv   must agree but for rope (dv->rope = 0), as must their tables' sizes
+ *   max_rows the most rows that a sequence has: rows of a sequence beyond it are left as they were
+ *   max_kv   the longest kv_len, or more: a bound by which the work is split (any value is right)
+ *   scale    finite, > 0
+ *   workspace  kvq_attend_paged_workspace_bytes() bytes, 256-byte aligned, contents irrelevant, not
+ *            shared by calls in flight at the same time
+ * Scores, softmax statistics and sums are held in fp32; the decoded keys and values and the softmax
+ * weights enter the products rounded to fp16, sinks enter in fp32. */
+kvq_status kvq_attend_paged(const kvq_desc* dk, const kvq_desc* dv, const void* q, int64_t q_stride, int32_t q_heads,
+                            const kvq_packed* k_cache, const kvq_tables* tk, const kvq_packed* v_cache,
+                            const kvq_tables* tv, const kvq_paged* pg, int32_t max_rows, int32_t max_kv, float scale,
+                            void* out, int64_t out_stride, void* workspace, size_t workspace_bytes,
+                            kvq_stream_t stream);
+
+/* Workspace bytes of kvq_attend_paged for these arguments; 0 if they are invalid or unsupported. */
+size_t kvq_attend_paged_workspace_bytes(const kvq_desc* dk, const kvq_desc* dv, int32_t q_heads, const kvq_paged* pg,
+                                        int32_t max_rows, int32_t max_kv);
+
+/* Element types of kvq_attend_prompt. */
+enum { KVQ_F16 = 0, KVQ_BF16 = 1 };
+
+/* Causal attention over whole packed prompts, before anything is compressed: row i of sequence s
+ * (rows cu_rows[s] .. cu_rows[s+1]-1) attends to the rows 0..i of its own sequence,
+ *   out[r][qh] = sum_{n <= i} softmax_n(scale * <q[r][qh], k_n>) v_n.
+ *   q, out   [n_rows][q_heads][head_dim], k, v [n_rows][heads][head_dim], of element type `dtype`
+ *            (KVQ_F16, KVQ_BF16), RoPE'd; *_stride elements between rows (multiples of 8), 16-byte
+ *            aligned, so slices of one fused projection can be given as they are
+ *   heads, q_heads  q_heads a multiple of heads, at most 128*heads; head_dim 64 or 128
+ *   cu_rows  int32 [n_seqs+1], device; rows behind cu_rows[n_seqs] are left as they were
+ *   max_rows the longest sequence's rows: rows of a sequence beyond it are left as they were
+ *   scale    finite, > 0
+ * Scores, statistics and sums are held in fp32, the weights enter the product with v rounded to
+ * `dtype`. What lies outside a row's view (later rows, other sequences, rows of no sequence) has no
+ * effect on it, infinities and NaN included. */
+kvq_status kvq_attend_prompt(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                             int64_t v_stride, int32_t n_seqs, int32_t n_rows, int32_t q_heads, int32_t heads,
+                             int32_t head_dim, int32_t dtype, const int32_t* cu_rows, int32_t max_rows, float scale,
+                             void* out, int64_t out_stride, kvq_stream_t stream);
+
 /* Channel permutation by abs-max ([RotateKV] outlier-aware rotation: channel reordering before
  * the FWHT). For each head h, a_j = max over the B batches and the positions t0..t0+T-1 that are
  * not sinks (position >= n_sink, or not in tb->sink_pos) of |y_j|, where y is the fp32 input of the permutation step:

@@ -20,12 +20,15 @@ LIB_PATH = os.path.join(_HERE, "libkvq.so")
 KVQ_OK, KVQ_ERR_INVALID, KVQ_ERR_UNSUPPORTED, KVQ_ERR_ALIGN, KVQ_ERR_CUDA, KVQ_ERR_TIMEOUT = range(6)
 KVQ_ROT_NONE, KVQ_ROT_FWHT_HEAD, KVQ_ROT_FWHT_GROUP, KVQ_ROT_ISO_SO4, KVQ_ROT_ISO_SO3 = range(5)
 KVQ_Q_MINMAX, KVQ_Q_CODEBOOK, KVQ_Q_CODEBOOK_DYN = 0, 1, 2
+KVQ_F16, KVQ_BF16 = 0, 1
 KVQ_FIELD_CODES, KVQ_FIELD_SCALE_ZERO, KVQ_FIELD_SINK, KVQ_FIELD_NORM, KVQ_FIELD_EXT = range(5)
 
 EXPORTED = ("kvq_encode", "kvq_decode", "kvq_score", "kvq_score_literal", "kvq_attend", "kvq_attend_noalloc", "kvq_attend_workspace_bytes",
             "kvq_calibrate_perm", "kvq_calibrate_workspace_bytes", "kvq_pair_energy",
             "kvq_detect_sinks", "kvq_detect_sinks_workspace_bytes",
             "kvq_calibrate_codebook", "kvq_calibrate_codebook_workspace_bytes",
+            "kvq_page_map", "kvq_encode_paged", "kvq_decode_paged", "kvq_attend_paged",
+            "kvq_attend_paged_workspace_bytes", "kvq_attend_prompt",
             "kvq_packed_bytes", "kvq_rope_table", "kvq_rope_table_ex", "kvq_lloyd_max_codebook", "kvq_check", "kvq_debug_expire_wait",
             "kvq_status_str", "kvq_version")
 
@@ -52,6 +55,11 @@ class KvqError(RuntimeError):
     def __init__(self, status: int, what: str = ""):
         self.status = status
         super().__init__(f"{what}: {kvq_status_str(status)} ({status})")
+
+
+class kvq_paged(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("n_seqs", "n_rows", "max_pages", "sink_rows")] + \
+               [(n, ctypes.c_void_p) for n in ("cu_rows", "kv_len", "block_table", "seq", "pos", "slot", "sink_slot")]
 
 
 def _load():
@@ -81,6 +89,15 @@ def _load():
     L.kvq_calibrate_workspace_bytes.restype = ctypes.c_size_t
     L.kvq_attend_workspace_bytes.argtypes = [P(kvq_desc), P(kvq_desc), i32, i32]
     L.kvq_attend_workspace_bytes.restype = ctypes.c_size_t
+    i64, f32, sz = ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
+    L.kvq_page_map.argtypes = [P(kvq_desc), P(kvq_paged), vp, vp, vp, i32, vp, vp, st]
+    L.kvq_encode_paged.argtypes = [P(kvq_desc), vp, i64, P(kvq_paged), P(kvq_tables), P(kvq_packed), st]
+    L.kvq_decode_paged.argtypes = [P(kvq_desc), P(kvq_packed), P(kvq_paged), P(kvq_tables), vp, i64, i32, st]
+    L.kvq_attend_paged.argtypes = [P(kvq_desc), P(kvq_desc), vp, i64, i32, P(kvq_packed), P(kvq_tables),
+                                   P(kvq_packed), P(kvq_tables), P(kvq_paged), i32, i32, f32, vp, i64, vp, sz, st]
+    L.kvq_attend_paged_workspace_bytes.argtypes = [P(kvq_desc), P(kvq_desc), i32, P(kvq_paged), i32, i32]
+    L.kvq_attend_paged_workspace_bytes.restype = sz
+    L.kvq_attend_prompt.argtypes = [vp, i64, vp, i64, vp, i64, i32, i32, i32, i32, i32, i32, vp, i32, f32, vp, i64, st]
     L.kvq_packed_bytes.argtypes = [P(kvq_desc), i32]
     L.kvq_packed_bytes.restype = ctypes.c_size_t
     L.kvq_rope_table.argtypes = [vp, i32, i32, ctypes.c_double]
@@ -93,6 +110,7 @@ def _load():
     L.kvq_version.restype = i32
     for n in ("kvq_encode", "kvq_decode", "kvq_score", "kvq_score_literal", "kvq_attend", "kvq_attend_noalloc", "kvq_calibrate_perm",
               "kvq_pair_energy", "kvq_detect_sinks", "kvq_calibrate_codebook",
+              "kvq_page_map", "kvq_encode_paged", "kvq_decode_paged", "kvq_attend_paged", "kvq_attend_prompt",
               "kvq_rope_table", "kvq_rope_table_ex",
               "kvq_lloyd_max_codebook",
               "kvq_check", "kvq_debug_expire_wait"):
@@ -140,6 +158,46 @@ def kvq_attend_noalloc(dk: kvq_desc, dv: kvq_desc, q: int, q_heads: int, k_cache
     return lib.kvq_attend_noalloc(ctypes.byref(dk), ctypes.byref(dv), q, q_heads, ctypes.byref(k_cache),
                                   ctypes.byref(tk), ctypes.byref(v_cache), ctypes.byref(tv), n_tokens, scale, out,
                                   stream)
+
+
+def kvq_page_map(desc: kvq_desc, batch: kvq_paged, ctx_len: int, new_len: int, free_pages: int, n_free: int,
+                 free_used: int, report: int, stream: int = 0) -> int:
+    return lib.kvq_page_map(ctypes.byref(desc), ctypes.byref(batch), ctx_len, new_len, free_pages, n_free, free_used,
+                            report, stream)
+
+
+def kvq_encode_paged(desc: kvq_desc, x: int, x_stride: int, batch: kvq_paged, tables: kvq_tables, out: kvq_packed,
+                     stream: int = 0) -> int:
+    return lib.kvq_encode_paged(ctypes.byref(desc), x, x_stride, ctypes.byref(batch), ctypes.byref(tables),
+                                ctypes.byref(out), stream)
+
+
+def kvq_decode_paged(desc: kvq_desc, packed: kvq_packed, batch: kvq_paged, tables: kvq_tables, x_out: int,
+                     x_stride: int, out_fp32: int, stream: int = 0) -> int:
+    return lib.kvq_decode_paged(ctypes.byref(desc), ctypes.byref(packed), ctypes.byref(batch), ctypes.byref(tables),
+                                x_out, x_stride, int(out_fp32), stream)
+
+
+def kvq_attend_paged(dk: kvq_desc, dv: kvq_desc, q: int, q_stride: int, q_heads: int, k_cache: kvq_packed,
+                     tk: kvq_tables, v_cache: kvq_packed, tv: kvq_tables, batch: kvq_paged, max_rows: int,
+                     max_kv: int, scale: float, out: int, out_stride: int, workspace: int, workspace_bytes: int,
+                     stream: int = 0) -> int:
+    return lib.kvq_attend_paged(ctypes.byref(dk), ctypes.byref(dv), q, q_stride, q_heads, ctypes.byref(k_cache),
+                                ctypes.byref(tk), ctypes.byref(v_cache), ctypes.byref(tv), ctypes.byref(batch),
+                                max_rows, max_kv, scale, out, out_stride, workspace, workspace_bytes, stream)
+
+
+def kvq_attend_paged_workspace_bytes(dk: kvq_desc, dv: kvq_desc, q_heads: int, batch: kvq_paged, max_rows: int,
+                                     max_kv: int) -> int:
+    return lib.kvq_attend_paged_workspace_bytes(ctypes.byref(dk), ctypes.byref(dv), q_heads, ctypes.byref(batch),
+                                                max_rows, max_kv)
+
+
+def kvq_attend_prompt(q: int, q_stride: int, k: int, k_stride: int, v: int, v_stride: int, n_seqs: int, n_rows: int,
+                      q_heads: int, heads: int, head_dim: int, dtype: int, cu_rows: int, max_rows: int, scale: float,
+                      out: int, out_stride: int, stream: int = 0) -> int:
+    return lib.kvq_attend_prompt(q, q_stride, k, k_stride, v, v_stride, n_seqs, n_rows, q_heads, heads, head_dim,
+                                 dtype, cu_rows, max_rows, scale, out, out_stride, stream)
 
 
 def kvq_calibrate_perm(d: kvq_desc, x: int, tb: kvq_tables, perm_out: int, workspace: int, workspace_bytes: int,

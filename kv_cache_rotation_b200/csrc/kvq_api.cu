@@ -416,6 +416,180 @@ kvq_status kvq_attend_noalloc(const kvq_desc* dk, const kvq_desc* dv, const void
                        reinterpret_cast<cudaStream_t>(stream), ctx);
 }
 
+namespace {
+// A paged cache's descriptor: pages of the pool, page size; min-max records of the head variant.
+kvq_status check_paged_desc(const kvq_desc* d, kvq_desc* out) {
+  if (!d) return KVQ_ERR_INVALID;
+  kvq_desc p = *d;
+  p.tokens = p.t0 = 0;
+  kvq_status s = check_desc(&p);
+  if (s != KVQ_OK) return s;
+  if ((p.rot != KVQ_ROT_NONE && p.rot != KVQ_ROT_FWHT_HEAD) || p.quant != KVQ_Q_MINMAX) return KVQ_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(p.batch) * p.t_cap >= (int64_t(1) << 31)) return KVQ_ERR_UNSUPPORTED;
+  *out = p;
+  return KVQ_OK;
+}
+
+// The sizes of a batch, and that its sinks have buffers when the cache keeps sinks.
+kvq_status check_paged(const kvq_desc& d, const kvq_paged* pg) {
+  if (!pg || pg->n_seqs < 0 || pg->n_rows < 0 || pg->max_pages <= 0 || pg->sink_rows < 0) return KVQ_ERR_INVALID;
+  if (d.n_sink > 0 && pg->sink_rows == 0 && pg->n_rows > 0) return KVQ_ERR_INVALID;
+  if (static_cast<int64_t>(pg->n_rows) * d.heads >= (int64_t(1) << 31)) return KVQ_ERR_UNSUPPORTED;
+  return KVQ_OK;
+}
+
+// Row maps of encode / decode, and the tables without a sink list.
+kvq_status check_rows(const kvq_desc& d, const kvq_paged& pg, const kvq_tables* tb, const kvq_packed* c,
+                      int64_t stride) {
+  if (!tb) return KVQ_ERR_INVALID;
+  if (d.n_sink > 0 && tb->sink_pos) return KVQ_ERR_UNSUPPORTED;
+  if (!pg.pos || !pg.slot || (d.n_sink > 0 && !pg.seq)) return KVQ_ERR_INVALID;
+  if (!aligned(pg.pos, 16) || !aligned(pg.slot, 16) || (pg.seq && !aligned(pg.seq, 16)) ||
+      (pg.sink_slot && !aligned(pg.sink_slot, 4)))
+    return KVQ_ERR_ALIGN;
+  if (stride < static_cast<int64_t>(d.heads) * d.head_dim) return KVQ_ERR_INVALID;
+  if (stride % 8) return KVQ_ERR_ALIGN;
+  kvq_status s = check_tables(&d, tb, 0);
+  return s != KVQ_OK ? s : check_packed(&d, c);
+}
+}  // namespace
+
+kvq_status kvq_page_map(const kvq_desc* d, const kvq_paged* pg, const int32_t* ctx_len, const int32_t* new_len,
+                        const int32_t* free_pages, int32_t n_free, const int32_t* free_used, int32_t* report,
+                        kvq_stream_t stream) {
+  kvq_desc p;
+  kvq_status s = check_paged_desc(d, &p);
+  if (s != KVQ_OK) return s;
+  p.n_sink = 0;
+  if ((s = check_paged(p, pg)) != KVQ_OK) return s;
+  if (pg->n_seqs > kMapMaxSeqs) return KVQ_ERR_UNSUPPORTED;
+  if (n_free < 0 || (n_free > 0 && !free_pages) || !free_used || !report) return KVQ_ERR_INVALID;
+  if (pg->n_seqs > 0 && (!ctx_len || !new_len || !pg->kv_len || !pg->block_table)) return KVQ_ERR_INVALID;
+  if (!pg->cu_rows || (pg->n_rows > 0 && (!pg->seq || !pg->pos || !pg->slot))) return KVQ_ERR_INVALID;
+  if (report == free_used) return KVQ_ERR_INVALID;
+  if (!aligned(pg->seq, 16) || !aligned(pg->pos, 16) || !aligned(pg->slot, 16) || !aligned(pg->cu_rows, 4) ||
+      !aligned(pg->kv_len, 4) || !aligned(pg->block_table, 4) || !aligned(ctx_len, 4) || !aligned(new_len, 4) ||
+      !aligned(free_pages, 4) || !aligned(free_used, 4) || !aligned(report, 4))
+    return KVQ_ERR_ALIGN;
+  LaunchCtx ctx;
+  if ((s = get_ctx(&ctx)) != KVQ_OK) return s;
+  return launch_page_map(p, *pg, ctx_len, new_len, free_pages, n_free, free_used, report,
+                         reinterpret_cast<cudaStream_t>(stream), ctx);
+}
+
+kvq_status kvq_encode_paged(const kvq_desc* d, const void* x, int64_t x_stride, const kvq_paged* pg,
+                            const kvq_tables* tb, const kvq_packed* out, kvq_stream_t stream) {
+  kvq_desc p;
+  kvq_status s = check_paged_desc(d, &p);
+  if (s != KVQ_OK || (s = check_paged(p, pg)) != KVQ_OK) return s;
+  if (!x) return KVQ_ERR_INVALID;
+  if (!aligned(x, 16)) return KVQ_ERR_ALIGN;
+  if ((s = check_rows(p, *pg, tb, out, x_stride)) != KVQ_OK) return s;
+  if (pg->n_rows == 0) return KVQ_OK;
+  LaunchCtx ctx;
+  if ((s = get_ctx(&ctx)) != KVQ_OK) return s;
+  return launch_encode_paged(p, x, x_stride, *pg, *tb, *out, reinterpret_cast<cudaStream_t>(stream), ctx);
+}
+
+kvq_status kvq_decode_paged(const kvq_desc* d, const kvq_packed* in, const kvq_paged* pg, const kvq_tables* tb,
+                            void* x_out, int64_t x_stride, int32_t out_fp32, kvq_stream_t stream) {
+  kvq_desc p;
+  kvq_status s = check_paged_desc(d, &p);
+  if (s != KVQ_OK || (s = check_paged(p, pg)) != KVQ_OK) return s;
+  if (!x_out || (out_fp32 != 0 && out_fp32 != 1)) return KVQ_ERR_INVALID;
+  if (!aligned(x_out, 16)) return KVQ_ERR_ALIGN;
+  if ((s = check_rows(p, *pg, tb, in, x_stride)) != KVQ_OK) return s;
+  if (pg->n_rows == 0) return KVQ_OK;
+  LaunchCtx ctx;
+  if ((s = get_ctx(&ctx)) != KVQ_OK) return s;
+  return launch_decode_paged(p, *in, *pg, *tb, x_out, x_stride, out_fp32, reinterpret_cast<cudaStream_t>(stream), ctx);
+}
+
+namespace {
+kvq_status check_attend_paged(const kvq_desc* dk, const kvq_desc* dv, int32_t q_heads, const kvq_paged* pg,
+                              int32_t max_rows, int32_t max_kv, kvq_desc* k_out, kvq_desc* v_out) {
+  kvq_status s = check_paged_desc(dk, k_out);
+  if (s != KVQ_OK || (s = check_paged_desc(dv, v_out)) != KVQ_OK) return s;
+  const kvq_desc &k = *k_out, &v = *v_out;
+  if (v.rope) return KVQ_ERR_UNSUPPORTED;
+  if (k.batch != v.batch || k.heads != v.heads || k.head_dim != v.head_dim || k.t_cap != v.t_cap ||
+      k.bits != v.bits || k.group != v.group || k.n_sink != v.n_sink || k.rot != v.rot || k.quant != v.quant)
+    return KVQ_ERR_INVALID;
+  if (q_heads <= 0 || q_heads % k.heads) return KVQ_ERR_INVALID;
+  if (q_heads / k.heads > 128 || k.heads > 65535) return KVQ_ERR_UNSUPPORTED;
+  if (max_rows < 0 || max_kv < 0) return KVQ_ERR_INVALID;
+  if ((s = check_paged(k, pg)) != KVQ_OK) return s;
+  if (static_cast<int64_t>(pg->n_rows) * q_heads >= (int64_t(1) << 31)) return KVQ_ERR_UNSUPPORTED;
+  return KVQ_OK;
+}
+
+bool good_scale(float scale) { return isfinite(scale) && scale > 0.0f; }
+}  // namespace
+
+size_t kvq_attend_paged_workspace_bytes(const kvq_desc* dk, const kvq_desc* dv, int32_t q_heads, const kvq_paged* pg,
+                                        int32_t max_rows, int32_t max_kv) {
+  kvq_desc k, v;
+  if (check_attend_paged(dk, dv, q_heads, pg, max_rows, max_kv, &k, &v) != KVQ_OK) return 0;
+  return attend_paged_workspace_bytes(k, q_heads, *pg, max_rows, max_kv);
+}
+
+kvq_status kvq_attend_paged(const kvq_desc* dk, const kvq_desc* dv, const void* q, int64_t q_stride, int32_t q_heads,
+                            const kvq_packed* k_cache, const kvq_tables* tk, const kvq_packed* v_cache,
+                            const kvq_tables* tv, const kvq_paged* pg, int32_t max_rows, int32_t max_kv, float scale,
+                            void* out, int64_t out_stride, void* workspace, size_t workspace_bytes,
+                            kvq_stream_t stream) {
+  kvq_desc k, v;
+  kvq_status s = check_attend_paged(dk, dv, q_heads, pg, max_rows, max_kv, &k, &v);
+  if (s != KVQ_OK) return s;
+  if (!q || !out || !workspace || !good_scale(scale)) return KVQ_ERR_INVALID;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(workspace, 256)) return KVQ_ERR_ALIGN;
+  if (q_stride < static_cast<int64_t>(q_heads) * k.head_dim || out_stride < static_cast<int64_t>(q_heads) * k.head_dim)
+    return KVQ_ERR_INVALID;
+  if (q_stride % 8 || out_stride % 8) return KVQ_ERR_ALIGN;
+  if (!tk || !tv) return KVQ_ERR_INVALID;
+  if (k.n_sink > 0 && (tk->sink_pos || tv->sink_pos)) return KVQ_ERR_UNSUPPORTED;
+  if ((s = check_tables(&k, tk, 0)) != KVQ_OK || (s = check_tables(&v, tv, 0)) != KVQ_OK) return s;
+  if ((s = check_packed(&k, k_cache)) != KVQ_OK || (s = check_packed(&v, v_cache)) != KVQ_OK) return s;
+  if (pg->n_seqs > 0 && (!pg->cu_rows || !pg->kv_len || !pg->block_table)) return KVQ_ERR_INVALID;
+  if (!aligned(pg->cu_rows, 4) || !aligned(pg->kv_len, 4) || !aligned(pg->block_table, 4) ||
+      !aligned(pg->sink_slot, 4))
+    return KVQ_ERR_ALIGN;
+  if (workspace_bytes < attend_paged_workspace_bytes(k, q_heads, *pg, max_rows, max_kv)) return KVQ_ERR_INVALID;
+  if (pg->n_rows == 0 || pg->n_seqs == 0 || max_rows == 0) return KVQ_OK;
+  LaunchCtx ctx;
+  if ((s = get_ctx(&ctx)) != KVQ_OK) return s;
+  return launch_attend_paged(k, v, q, q_stride, q_heads, *k_cache, *tk, *v_cache, *tv, *pg, max_rows, max_kv, scale,
+                             out, out_stride, workspace, reinterpret_cast<cudaStream_t>(stream), ctx);
+}
+
+kvq_status kvq_attend_prompt(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                             int64_t v_stride, int32_t n_seqs, int32_t n_rows, int32_t q_heads, int32_t heads,
+                             int32_t head_dim, int32_t dtype, const int32_t* cu_rows, int32_t max_rows, float scale,
+                             void* out, int64_t out_stride, kvq_stream_t stream) {
+  if (n_seqs < 0 || n_rows < 0 || q_heads <= 0 || heads <= 0 || q_heads % heads || max_rows < 0) return KVQ_ERR_INVALID;
+  if (dtype != KVQ_F16 && dtype != KVQ_BF16) return KVQ_ERR_INVALID;
+  if (head_dim != 64 && head_dim != 128) return KVQ_ERR_UNSUPPORTED;
+  if (q_heads / heads > 128 || heads > 65535) return KVQ_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(n_rows) * q_heads >= (int64_t(1) << 31)) return KVQ_ERR_UNSUPPORTED;
+  if (!good_scale(scale)) return KVQ_ERR_INVALID;
+  if (!q || !k || !v || !out || !cu_rows) return KVQ_ERR_INVALID;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) || !aligned(cu_rows, 4))
+    return KVQ_ERR_ALIGN;
+  const int64_t qw = static_cast<int64_t>(q_heads) * head_dim, kw = static_cast<int64_t>(heads) * head_dim;
+  if (q_stride < qw || out_stride < qw || k_stride < kw || v_stride < kw) return KVQ_ERR_INVALID;
+  if (q_stride % 8 || out_stride % 8 || k_stride % 8 || v_stride % 8) return KVQ_ERR_ALIGN;
+  // a tensor map's row stride stays below 2^40 bytes
+  const int64_t far = int64_t(1) << 38;
+  if (q_stride > far || out_stride > far || k_stride > far || v_stride > far) return KVQ_ERR_UNSUPPORTED;
+  if (n_seqs == 0 || n_rows == 0 || max_rows == 0) return KVQ_OK;
+  LaunchCtx ctx;
+  const kvq_status s = get_ctx(&ctx);
+  if (s != KVQ_OK) return s;
+  const PromptArgs p{q, k, v, out, q_stride, k_stride, v_stride, out_stride, n_seqs, n_rows, q_heads, heads,
+                     head_dim, dtype == KVQ_BF16, max_rows, cu_rows, scale};
+  return launch_attend_prompt(p, reinterpret_cast<cudaStream_t>(stream), ctx);
+}
+
 kvq_status kvq_pair_energy(const kvq_desc* d, const void* x, uint64_t* energy_out, int16_t* rank_out,
                            kvq_stream_t stream) {
   kvq_status s = check_desc(d);

@@ -76,6 +76,31 @@ kvq_status launch_attend(const kvq_desc& dk, const kvq_desc& dv, const void* q, 
                          const kvq_packed& kc, const kvq_tables& tk, const kvq_packed& vc, const kvq_tables& tv,
                          int n_tokens, float scale, float* out, void* ws, cudaStream_t st, const LaunchCtx& ctx);
 
+// The paged cache (kvq_pages.cu, kvq_attend_paged.cu) and whole prompts (kvq_prompt.cu).
+constexpr int kMapMaxSeqs = 16384;  // sequences of one kvq_page_map call
+kvq_status launch_page_map(const kvq_desc& d, const kvq_paged& pg, const int32_t* ctx_len, const int32_t* new_len,
+                           const int32_t* free_pages, int n_free, const int32_t* free_used, int32_t* report,
+                           cudaStream_t st, const LaunchCtx& ctx);
+kvq_status launch_encode_paged(const kvq_desc& d, const void* x, int64_t stride, const kvq_paged& pg,
+                               const kvq_tables& tb, const kvq_packed& out, cudaStream_t st, const LaunchCtx& ctx);
+kvq_status launch_decode_paged(const kvq_desc& d, const kvq_packed& in, const kvq_paged& pg, const kvq_tables& tb,
+                               void* x_out, int64_t stride, int out_fp32, cudaStream_t st, const LaunchCtx& ctx);
+size_t attend_paged_workspace_bytes(const kvq_desc& dk, int q_heads, const kvq_paged& pg, int max_rows, int max_kv);
+kvq_status launch_attend_paged(const kvq_desc& dk, const kvq_desc& dv, const void* q, int64_t q_stride, int q_heads,
+                               const kvq_packed& kc, const kvq_tables& tk, const kvq_packed& vc, const kvq_tables& tv,
+                               const kvq_paged& pg, int max_rows, int max_kv, float scale, void* out,
+                               int64_t out_stride, void* ws, cudaStream_t st, const LaunchCtx& ctx);
+// q, k, v, out and their row strides, as kvq_attend_prompt takes them.
+struct PromptArgs {
+  const void *q, *k, *v;
+  void* out;
+  int64_t q_stride, k_stride, v_stride, out_stride;
+  int n_seqs, n_rows, q_heads, heads, head_dim, bf16, max_rows;
+  const int32_t* cu_rows;
+  float scale;
+};
+kvq_status launch_attend_prompt(const PromptArgs& p, cudaStream_t st, const LaunchCtx& ctx);
+
 // cudaFuncSetAttribute(MaxDynamicSharedMemorySize) only when a kernel needs
 // more dynamic shared memory on this device than it was last granted (the
 // attribute persists per device). A small per-thread cache of (kernel,

@@ -13,10 +13,10 @@ from typing import Optional
 
 import torch
 
-from . import (KVQ_FIELD_CODES, KVQ_FIELD_EXT, KVQ_FIELD_NORM, KVQ_FIELD_SCALE_ZERO, KVQ_FIELD_SINK,
+from . import (KVQ_BF16, KVQ_F16, KVQ_FIELD_CODES, KVQ_FIELD_EXT, KVQ_FIELD_NORM, KVQ_FIELD_SCALE_ZERO, KVQ_FIELD_SINK,
                KVQ_Q_CODEBOOK, KVQ_Q_CODEBOOK_DYN, KVQ_Q_MINMAX, KVQ_ROT_FWHT_GROUP, KVQ_ROT_FWHT_HEAD, KVQ_ROT_ISO_SO3, KVQ_ROT_ISO_SO4, KVQ_ROT_NONE,
                check,
-               kvq_decode, kvq_desc, kvq_encode, kvq_lloyd_max_codebook, kvq_packed, kvq_packed_bytes,
+               kvq_decode, kvq_desc, kvq_encode, kvq_paged, kvq_lloyd_max_codebook, kvq_packed, kvq_packed_bytes,
                kvq_rope_table, kvq_score, kvq_score_literal, kvq_tables)
 
 ROT = {"none": KVQ_ROT_NONE, "fwht_head": KVQ_ROT_FWHT_HEAD, "fwht_group": KVQ_ROT_FWHT_GROUP,
@@ -369,6 +369,229 @@ def bind_attend(dk: kvq_desc, dv: kvq_desc, q: torch.Tensor, k_packed: Packed, t
         check(lib.kvq_attend(*args), "kvq_attend")
     call.keep = keep
     return call
+
+
+# ---------------------------------------------------------------- the paged cache
+@dataclass
+class Paged:
+    """A ragged batch over a paged cache (kvq_paged): int32 device tensors, filled by page_map or by
+    the caller. What a call does not read may be None (the row maps for attend_paged, the lengths
+    and the table for encode_paged and decode_paged)."""
+    cu_rows: Optional[torch.Tensor] = None      # [S+1]
+    kv_len: Optional[torch.Tensor] = None       # [S]
+    block_table: Optional[torch.Tensor] = None  # [S][max_pages]
+    seq: Optional[torch.Tensor] = None          # [n_rows]
+    pos: Optional[torch.Tensor] = None          # [n_rows]
+    slot: Optional[torch.Tensor] = None         # [n_rows]
+    sink_slot: Optional[torch.Tensor] = None    # [S]: rows of the sink buffers (None: row s)
+
+    def struct(self, n_rows: int = None, sink: Optional[torch.Tensor] = None) -> kvq_paged:
+        S = None
+        for t, name in ((self.kv_len, "kv_len"), (self.cu_rows, "cu_rows"), (self.block_table, "block_table"),
+                        (self.sink_slot, "sink_slot")):
+            if t is not None:
+                n = t.shape[0] - (1 if name == "cu_rows" else 0)
+                _req(t, name, (torch.int32,))
+                if t.dim() != (2 if name == "block_table" else 1) or n < 0 or S not in (None, n):
+                    raise ValueError(f"{name}: shape {tuple(t.shape)} does not fit {S} sequences")
+                S = n
+        for t, name in ((self.seq, "seq"), (self.pos, "pos"), (self.slot, "slot")):
+            if t is not None:
+                if n_rows is None:
+                    n_rows = t.numel()
+                _req(t, name, (torch.int32,), (n_rows,))
+        p = kvq_paged()
+        p.n_seqs, p.n_rows = S or 0, n_rows or 0
+        p.max_pages = self.block_table.shape[1] if self.block_table is not None else 1
+        p.sink_rows = sink.shape[0] if sink is not None else 0
+        for name in ("cu_rows", "kv_len", "block_table", "seq", "pos", "slot", "sink_slot"):
+            t = getattr(self, name)
+            setattr(p, name, t.data_ptr() if t is not None else None)
+        return p
+
+
+def make_paged(n_seqs: int, n_rows: int, max_pages: int, block_table: torch.Tensor = None, sink_slot=None,
+               device="cuda") -> Paged:
+    """The arrays of a batch for page_map to fill (an empty block table is one of -1)."""
+    def ints(*shape):
+        return torch.empty(shape, dtype=torch.int32, device=device)
+    if block_table is None:
+        block_table = torch.full((n_seqs, max_pages), -1, dtype=torch.int32, device=device)
+    return Paged(ints(n_seqs + 1), ints(n_seqs), block_table, ints(n_rows), ints(n_rows), ints(n_rows), sink_slot)
+
+
+def alloc_paged(d: kvq_desc, sink_rows: int = 0, device="cuda", zero=True) -> Packed:
+    """The buffers of a paged cache: d.batch pages of d.t_cap tokens, and the fp16 sinks of
+    sink_rows sequences."""
+    n_sink, d.n_sink = d.n_sink, 0
+    try:
+        p = alloc_packed(d, device, zero)
+    finally:
+        d.n_sink = n_sink
+    if n_sink:
+        p.sink = (torch.zeros if zero else torch.empty)((sink_rows, d.heads, n_sink, d.head_dim), dtype=torch.float16,
+                                                        device=device)
+    return p
+
+
+def _here(*tensors) -> None:
+    """The library launches on the current device: its tensors have to be there."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != dev:
+            raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{dev}")
+
+
+def _rows(t: torch.Tensor, name: str, dtypes, heads=None, dim=None) -> int:
+    """Elements between the packed rows of t [n_rows][heads][dim]; the rows themselves are dense."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be a CUDA tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected one of {dtypes}")
+    if t.dim() != 3 or (heads is not None and t.shape[1] != heads) or (dim is not None and t.shape[2] != dim):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected (n_rows, {heads or 'heads'}, {dim or 'head_dim'})")
+    if (t.stride(2) != 1 and t.shape[2] > 1) or (t.stride(1) != t.shape[2] and t.shape[1] > 1):
+        raise ValueError(f"{name}: the heads of a row must be dense")
+    if t.shape[0] <= 1:  # a single row has any stride
+        return -(-t.shape[1] * t.shape[2] // 8) * 8
+    return int(t.stride(0))
+
+
+def _call(name: str, args: tuple, keep: tuple, stream):
+    """A zero-argument call of the entry point `name`: on `stream`, or on the stream that is current
+    when it is called (so a bound call can be captured)."""
+    from . import lib
+    fn, keep_stream = getattr(lib, name), None if stream is None else _stream(stream)
+
+    def call():
+        check(fn(*args, _stream(None) if keep_stream is None else keep_stream), name)
+    call.keep = keep
+    return call
+
+
+def bind_page_map(d: kvq_desc, batch: Paged, ctx_len: torch.Tensor, new_len: torch.Tensor, free_pages: torch.Tensor,
+                  free_used: torch.Tensor, report: torch.Tensor, stream=None):
+    p = batch.struct()
+    for name in ("cu_rows", "kv_len", "block_table", "seq", "pos", "slot"):
+        if getattr(batch, name) is None:
+            raise ValueError(f"{name}: page_map fills it")
+    _req(ctx_len, "ctx_len", (torch.int32,), (p.n_seqs,))
+    _req(new_len, "new_len", (torch.int32,), (p.n_seqs,))
+    _req(free_pages, "free_pages", (torch.int32,), (free_pages.numel(),))
+    _req(free_used, "free_used", (torch.int32,), (1,))
+    _req(report, "report", (torch.int32,), (4,))
+    if report.data_ptr() <= free_used.data_ptr() < report.data_ptr() + 16:
+        raise ValueError("report: must not overlap free_used")
+    _here(batch.cu_rows, batch.block_table, batch.seq, ctx_len, new_len, free_pages, free_used, report)
+    args = (ctypes.byref(d), ctypes.byref(p), ctx_len.data_ptr(), new_len.data_ptr(), free_pages.data_ptr(),
+            free_pages.numel(), free_used.data_ptr(), report.data_ptr())
+    return _call("kvq_page_map", args, (d, p, batch, ctx_len, new_len, free_pages, free_used, report), stream)
+
+
+def page_map(d: kvq_desc, batch: Paged, ctx_len: torch.Tensor, new_len: torch.Tensor, free_pages: torch.Tensor,
+             free_used: torch.Tensor, report: torch.Tensor = None, stream=None) -> torch.Tensor:
+    """Fill the batch from its lengths (kvq_page_map); returns the report, int32 [4]: rows, free pages
+    taken in all, rows without a slot, pages that were lacking. report[1:2] is the next call's free_used."""
+    if report is None:
+        report = torch.empty(4, dtype=torch.int32, device=ctx_len.device)
+    bind_page_map(d, batch, ctx_len, new_len, free_pages, free_used, report, stream)()
+    return report
+
+
+def bind_encode_paged(d: kvq_desc, x: torch.Tensor, batch: Paged, tables: Tables, packed: Packed, stream=None):
+    stride = _rows(x, "x", (torch.float16,), d.heads, d.head_dim)
+    p, tb, pk = batch.struct(x.shape[0], packed.sink), tables.struct(), packed.struct()
+    _here(x, batch.slot, packed.codes)
+    args = (ctypes.byref(d), x.data_ptr(), stride, ctypes.byref(p), ctypes.byref(tb), ctypes.byref(pk))
+    return _call("kvq_encode_paged", args, (d, x, batch, tables, packed, p, tb, pk), stream)
+
+
+def encode_paged(d: kvq_desc, x: torch.Tensor, batch: Paged, tables: Tables, packed: Packed, stream=None) -> None:
+    """Encode the rows x fp16 [n_rows][H][D] (dense heads, any row stride) into their slots."""
+    bind_encode_paged(d, x, batch, tables, packed, stream)()
+
+
+def bind_decode_paged(d: kvq_desc, packed: Packed, batch: Paged, tables: Tables, out: torch.Tensor, stream=None):
+    stride = _rows(out, "out", (torch.float16, torch.float32), d.heads, d.head_dim)
+    p, tb, pk = batch.struct(out.shape[0], packed.sink), tables.struct(), packed.struct()
+    _here(out, batch.slot, packed.codes)
+    args = (ctypes.byref(d), ctypes.byref(pk), ctypes.byref(p), ctypes.byref(tb), out.data_ptr(), stride,
+            1 if out.dtype == torch.float32 else 0)
+    return _call("kvq_decode_paged", args, (d, packed, batch, tables, out, p, tb, pk), stream)
+
+
+def decode_paged(d: kvq_desc, packed: Packed, batch: Paged, tables: Tables, out: torch.Tensor, stream=None) -> None:
+    """Decode the rows' records into out fp16 / fp32 [n_rows][H][D]; rows without a slot stay as they are."""
+    bind_decode_paged(d, packed, batch, tables, out, stream)()
+
+
+def attend_paged_workspace(dk: kvq_desc, dv: kvq_desc, q_heads: int, batch: Paged, max_rows: int, max_kv: int,
+                           n_rows: int = None) -> torch.Tensor:
+    """A workspace tensor for attend_paged; n_rows: the rows of q where the batch has no row maps."""
+    from . import kvq_attend_paged_workspace_bytes
+    p = batch.struct(n_rows)
+    p.sink_rows = 1 << 30  # sizes alone count here
+    nb = kvq_attend_paged_workspace_bytes(dk, dv, q_heads, p, max_rows, max_kv)
+    if nb == 0:
+        raise ValueError("kvq_attend_paged: invalid or unsupported shapes")
+    return torch.empty(nb, dtype=torch.uint8, device=batch.cu_rows.device)
+
+
+def bind_attend_paged(dk: kvq_desc, dv: kvq_desc, q: torch.Tensor, k_packed: Packed, tk: Tables, v_packed: Packed,
+                      tv: Tables, batch: Paged, max_rows: int, max_kv: int, scale: float, out: torch.Tensor,
+                      workspace: torch.Tensor, stream=None):
+    qs = _rows(q, "q", (torch.float16,), None, dk.head_dim)
+    os = _rows(out, "out", (torch.float16,), q.shape[1], dk.head_dim)
+    if out.shape[0] != q.shape[0]:
+        raise ValueError(f"out: {out.shape[0]} rows, expected {q.shape[0]}")
+    _req(workspace, "workspace", (torch.uint8,))
+    if (k_packed.sink is None) != (v_packed.sink is None) or \
+            (k_packed.sink is not None and k_packed.sink.shape != v_packed.sink.shape):
+        raise ValueError("sink: the two caches keep the sinks of the same sequences")
+    p = batch.struct(q.shape[0], k_packed.sink)
+    kp, vp, tks, tvs = k_packed.struct(), v_packed.struct(), tk.struct(), tv.struct()
+    _here(q, out, workspace, batch.block_table, k_packed.codes, v_packed.codes)
+    args = (ctypes.byref(dk), ctypes.byref(dv), q.data_ptr(), qs, q.shape[1], ctypes.byref(kp), ctypes.byref(tks),
+            ctypes.byref(vp), ctypes.byref(tvs), ctypes.byref(p), max_rows, max_kv, scale, out.data_ptr(), os,
+            workspace.data_ptr(), workspace.numel())
+    keep = (dk, dv, q, k_packed, tk, v_packed, tv, batch, out, workspace, p, kp, vp, tks, tvs)
+    return _call("kvq_attend_paged", args, keep, stream)
+
+
+def attend_paged(dk: kvq_desc, dv: kvq_desc, q: torch.Tensor, k_packed: Packed, tk: Tables, v_packed: Packed,
+                 tv: Tables, batch: Paged, max_rows: int, max_kv: int, scale: float, out: torch.Tensor,
+                 workspace: torch.Tensor, stream=None) -> None:
+    """Causal attention of each sequence's new rows q fp16 [n_rows][q_heads][D] over its pages."""
+    bind_attend_paged(dk, dv, q, k_packed, tk, v_packed, tv, batch, max_rows, max_kv, scale, out, workspace, stream)()
+
+
+def bind_attend_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_rows: torch.Tensor, max_rows: int,
+                       scale: float, out: torch.Tensor, stream=None):
+    qs = _rows(q, "q", (torch.float16, torch.bfloat16))
+    n, hq, dim = q.shape
+    ks, vs = _rows(k, "k", (q.dtype,), None, dim), _rows(v, "v", (q.dtype,), k.shape[1], dim)
+    os = _rows(out, "out", (q.dtype,), hq, dim)
+    if not (k.shape[0] == v.shape[0] == out.shape[0] == n):
+        raise ValueError("q, k, v and out must have the same rows")
+    _req(cu_rows, "cu_rows", (torch.int32,))
+    if cu_rows.dim() != 1 or cu_rows.numel() < 1:
+        raise ValueError(f"cu_rows: shape {tuple(cu_rows.shape)}, expected (sequences + 1,)")
+    _here(q, k, v, out, cu_rows)
+    args = (q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, cu_rows.numel() - 1, n, hq, k.shape[1], dim,
+            KVQ_BF16 if q.dtype == torch.bfloat16 else KVQ_F16, cu_rows.data_ptr(), max_rows, scale, out.data_ptr(), os)
+    return _call("kvq_attend_prompt", args, (q, k, v, cu_rows, out), stream)
+
+
+def attend_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_rows: torch.Tensor, max_rows: int,
+                  scale: float, out: torch.Tensor = None, stream=None) -> torch.Tensor:
+    """Causal attention over packed prompts: q, out [n_rows][q_heads][D], k, v [n_rows][heads][D], all
+    fp16 or all bf16, cu_rows int32 [S+1]."""
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    bind_attend_prompt(q, k, v, cu_rows, max_rows, scale, out, stream)()
+    return out
 
 
 # ---------------------------------------------------------------- pre-bound calls
