@@ -1,84 +1,337 @@
 // Causal attention over whole packed prompts (kvq_attend_prompt):
 //   out_i = sum_{n <= i} p_n v_n,  p = softmax_n(scale * q_i . k_n)
 // in one pass over the keys with the running maximum and sum of the softmax.
-#include <cuda_bf16.h>
+//
+// A CTA takes 2 x 128 query rows of one KV head: two slots of T = 128 / g
+// tokens, the g query heads of the KV head side by side (row t * g + j of a
+// slot is token t, head j), so a tile of keys serves every head that shares it
+// and a short prompt still fills the rows. Keys and values come in tiles of
+// 128 through one ring of TMA loads. Per tile and slot: scores = Q . K^T on
+// the tensor cores into tensor memory, softmax by a warpgroup (a thread per
+// row), the weights back into tensor memory in the scores' place, sums += P . V.
+// The two slots alternate: while one's scores are in the softmax, the tensor
+// cores work for the other.
+//
+// Warps: 0-3 and 4-7 softmax of slots 0 and 1; 8 loads; 9 issues the products;
+// 10 clears what the mask hides in V (see below).
+//
+// Masked keys get weight 0, but 0 * inf is not 0, so V must be finite wherever
+// a weight is masked: only the last tiles of a CTA (from the diagonal on) hold
+// masked keys, and warp 10 goes over those: rows behind the sequence become
+// zero, and a value that is not finite is taken out and its first row noted
+// per channel, by kind; the rows that see it get it back at the end.
 #include <math.h>
 
-#include "kvq_device.cuh"
+#include "kvq_flash.cuh"
 #include "kvq_internal.h"
 
 namespace kvq {
 namespace {
 
-template <typename T>
-__device__ __forceinline__ float2 to_f2(uint32_t w);
-template <>
-__device__ __forceinline__ float2 to_f2<__half>(uint32_t w) { return __half22float2(*reinterpret_cast<__half2*>(&w)); }
-template <>
-__device__ __forceinline__ float2 to_f2<__nv_bfloat16>(uint32_t w) { return __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&w)); }
+constexpr int kThreads = 384;  // three warpgroups; warp 11 is idle
+constexpr int kEdges = 4;  // tiles of a CTA that can hold masked keys: 256 rows, not aligned to the tiles
 
-// One warp per (row, query head), a lane per D / 32 channels.
+template <int D>
+struct Cfg {
+  static constexpr int kStages = D == 128 ? 5 : 10;
+  static constexpr uint32_t kHead = D / 64 * kTileBytes;  // 128 rows of a head
+  static constexpr uint32_t kRing = 2 * kHead;             // after the two Q tiles
+  static constexpr uint32_t kMisc = kRing + kStages * kHead;
+  static constexpr uint32_t kSmem = kMisc + 2048 + 1024;   // + alignment of the tiles
+};
+
+struct Misc {
+  uint64_t q_full, full[10], empty[10], s_full[2], p_full[2], o_full[2], loaded[kEdges], clean[kEdges];
+  uint32_t tmem;
+  int row0, len, q0, dirty;
+  int first[3][128];  // first row with +inf, -inf, NaN in a channel of V, relative to the sequence
+};
+static_assert(sizeof(Misc) <= 2048, "fits behind the ring");
+
+struct KernelArgs {
+  PromptArgs p;
+  int g, T;
+  uint32_t* err;
+  uint64_t wait_ns;
+  float mul;  // scale * log2(e)
+};
+
+// Item `idx` of KV-head-independent tiles, counted from the last sequence's last tile backwards: long
+// rows first. One warp; the result is in `m` (len 0: none).
+__device__ __forceinline__ void find_item(const PromptArgs& p, int TT, int idx, int lane, Misc* m) {
+  if (lane == 0) m->len = 0;
+  __syncwarp();
+  for (int s0 = p.n_seqs - 1; s0 >= 0; s0 -= 32) {
+    const int s = s0 - lane;
+    int b = 0, len = 0;
+    if (s >= 0) {
+      b = min(max(__ldg(p.cu_rows + s), 0), p.n_rows);
+      const int e = min(max(__ldg(p.cu_rows + s + 1), b), p.n_rows);
+      len = min(e - b, p.max_rows);
+    }
+    const int nt = (len + TT - 1) / TT;
+    int acc = nt;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, acc, o);
+      if (lane >= o) acc += y;
+    }
+    if (idx >= acc - nt && idx < acc) {
+      m->row0 = b;
+      m->len = len;
+      m->q0 = (nt - 1 - (idx - (acc - nt))) * TT;
+    }
+    const int total = __shfl_sync(0xffffffffu, acc, 31);
+    if (idx < total) break;
+    idx -= total;
+  }
+}
+
 template <typename T, int D>
-__global__ void __launch_bounds__(256) k_prompt_rows(const PromptArgs a) {
-  constexpr int W = D / 64;  // 32-bit words per lane
-  const int lane = threadIdx.x & 31;
-  const long long wi = blockIdx.x * 8ll + (threadIdx.x >> 5);
-  const int row = static_cast<int>(wi / a.q_heads), qh = static_cast<int>(wi % a.q_heads);
-  if (row >= a.n_rows) return;
-  int r0 = -1;
-  for (int s = 0; s < a.n_seqs; ++s) {
-    const int b = __ldg(a.cu_rows + s), e = __ldg(a.cu_rows + s + 1);
-    if (row >= b && row < e && row - b < a.max_rows) r0 = max(b, 0);
+__global__ void __launch_bounds__(kThreads, 1)
+    k_prompt_tiles(const KernelArgs a, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                   const __grid_constant__ CUtensorMap mv) {
+  using C = Cfg<D>;
+  constexpr int ST = C::kStages;
+  extern __shared__ uint8_t flash_smem[];
+  const uint32_t base = (smem_u32(flash_smem) + 1023u) & ~1023u;
+  uint8_t* const gbase = flash_smem + (base - smem_u32(flash_smem));
+  Misc* const m = reinterpret_cast<Misc*>(gbase + C::kMisc);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int idx = static_cast<int>(blockIdx.x / static_cast<unsigned>(a.p.heads));
+  const int h = static_cast<int>(blockIdx.x) - idx * a.p.heads;
+  const int TT = 2 * a.T;
+
+  if (warp == 8) find_item(a.p, TT, idx, lane, m);
+  __syncthreads();
+  const int row0 = m->row0, len = m->len, q0 = m->q0;
+  if (len == 0) return;
+  if (warp == 9) tmem_alloc(&m->tmem, 512);
+  if (tid == 0) {
+    mbar_init(&m->q_full, 1);
+    for (int i = 0; i < ST; ++i) mbar_init(&m->full[i], 1), mbar_init(&m->empty[i], 1);
+    for (int t = 0; t < 2; ++t) mbar_init(&m->s_full[t], 1), mbar_init(&m->p_full[t], 4), mbar_init(&m->o_full[t], 1);
+    for (int i = 0; i < kEdges; ++i) mbar_init(&m->loaded[i], 1), mbar_init(&m->clean[i], 1);
+    m->dirty = 0;
+    fence_mbar_init();
   }
-  if (r0 < 0) return;
-  const int h = qh / (a.q_heads / a.heads);
-  float q[2 * W], o[2 * W], m = -INFINITY, l = 0.0f;
-  const uint32_t* qp = reinterpret_cast<const uint32_t*>(static_cast<const T*>(a.q) + row * a.q_stride + qh * D) + lane * W;
+  if (tid < 128) m->first[0][tid] = m->first[1][tid] = m->first[2][tid] = 0x7fffffff;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = m->tmem;
+  const uint32_t ring = base + C::kRing;
+  // tiles of keys that slot t sees
+  int n_t[2];
 #pragma unroll
-  for (int i = 0; i < W; ++i) {
-    const float2 f = to_f2<T>(qp[i]);
-    q[2 * i] = f.x, q[2 * i + 1] = f.y;
-    o[2 * i] = o[2 * i + 1] = 0.0f;
+  for (int t = 0; t < 2; ++t) {
+    const int b = q0 + t * a.T, e = min(len, b + a.T);
+    n_t[t] = b < len ? (e + 127) >> 7 : 0;
   }
-  for (int n = r0; n <= row; ++n) {
-    const uint32_t* kp = reinterpret_cast<const uint32_t*>(static_cast<const T*>(a.k) + n * a.k_stride + h * D) + lane * W;
-    float s = 0.0f;
-#pragma unroll
-    for (int i = 0; i < W; ++i) {
-      const float2 f = to_f2<T>(__ldg(kp + i));
-      s = fmaf(q[2 * i], f.x, fmaf(q[2 * i + 1], f.y, s));
+  const int n = max(n_t[0], n_t[1]);
+  const int edge = (q0 + 1) >> 7;  // tiles from here on hold keys that some row does not see
+
+  // 168 registers a thread at launch, 64512 in all: 208 for the softmax, 80 for the rest (63488)
+  if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    const int t = warp >> 2;
+    const int r = tid & 127, tok = q0 + t * a.T + r / a.g, j = r % a.g;
+    const bool mine = r < a.T * a.g && tok < len;
+    const int lim = mine ? tok + 1 : 0x7fffffff;  // a row of no token is computed unmasked and not stored
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>(warp & 3) << 21);
+    const uint32_t s_addr = lane_base + 128 * t, o_addr = lane_base + 256 + D * t;
+    RowStat st;
+    bool ok = true;
+    for (int i = 0; i < n_t[t]; ++i) {
+      ok = mbar_wait(&m->s_full[t], i & 1, a.wait_ns, a.err);
+      if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+      tc_fence_after();
+      const int left = lim - 128 * i;  // columns seen
+      if (__any_sync(0xffffffffu, left < 128))
+        softmax_tile<T, D, true>(s_addr, o_addr, i > 0, a.mul, st, [&](int c) { return c < left; });
+      else
+        softmax_tile<T, D, false>(s_addr, o_addr, i > 0, a.mul, st, [](int) { return true; });
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&m->p_full[t]);
     }
+    if (ok && n_t[t] > 0) ok = __all_sync(0xffffffffu, mbar_wait(&m->o_full[t], 0, a.wait_ns, a.err));
+    if (ok && n_t[t] > 0) {
+      tc_fence_after();
+      const float inv = st.l > 0.0f || st.l != st.l ? 1.0f / st.l : 0.0f;
+      const bool dirty = *reinterpret_cast<volatile int*>(&m->dirty) != 0;
+      T* out = static_cast<T*>(a.p.out) + (static_cast<int64_t>(row0) + tok) * a.p.out_stride + (h * a.g + j) * D;
 #pragma unroll
-    for (int w = 16; w >= 1; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
-    s *= a.scale;
-    const float mn = fmaxf(m, s), f = m == mn ? 1.0f : __expf(m - mn), p = __expf(s - mn);
-    m = mn;
-    l = fmaf(l, f, p);
-    const uint32_t* vp = reinterpret_cast<const uint32_t*>(static_cast<const T*>(a.v) + n * a.v_stride + h * D) + lane * W;
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t o[32], w[16];
+        tmem_ld32(o_addr + 32 * c, o);
+        tmem_wait_ld32(o);
 #pragma unroll
-    for (int i = 0; i < W; ++i) {
-      const float2 v = to_f2<T>(__ldg(vp + i));
-      o[2 * i] = fmaf(o[2 * i], f, p * v.x);
-      o[2 * i + 1] = fmaf(o[2 * i + 1], f, p * v.y);
+        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * inv);
+        if (dirty) {  // the values taken out of V that this row sees
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            float x = __uint_as_float(o[i]);
+            if (m->first[0][32 * c + i] <= tok) x += INFINITY;
+            if (m->first[1][32 * c + i] <= tok) x -= INFINITY;
+            if (m->first[2][32 * c + i] <= tok) x = NAN;
+            o[i] = __float_as_uint(x);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) w[i] = Elem<T>::pack(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]));
+        if (mine) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            reinterpret_cast<uint4*>(out + 32 * c)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        }
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+  }
+  if (warp == 8) {
+    if (lane == 0) {  // tiles in the order K0 V0 K1 V1 ...
+      const uint32_t qbytes = static_cast<uint32_t>(a.T * a.g) * 128u * (D / 64);
+      mbar_arrive_expect_tx(&m->q_full, 2 * qbytes);
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c)
+          tma_load_3d(gbase + t * C::kHead + c * kTileBytes, &mq, 64 * c, h * a.g, row0 + q0 + t * a.T, &m->q_full);
+      // V from the diagonal on lands on a barrier of its own, used once: warp 10 has not followed the ring's
+      // phases. No stage is used again behind such a tile (at most three of them, five stages).
+      auto landed = [&](int i) {
+        return (i & 1) && (i >> 1) >= edge ? &m->loaded[(i >> 1) - edge] : &m->full[i % ST];
+      };
+      int i = 0;
+      for (; i < 2 * n; ++i) {
+        const int s = i % ST;
+        if (i >= ST && !mbar_wait(&m->empty[s], ((i / ST) & 1) ^ 1, a.wait_ns, a.err)) break;
+        mbar_arrive_expect_tx(landed(i), C::kHead);
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c)
+          tma_load_3d(gbase + C::kRing + s * C::kHead + c * kTileBytes, (i & 1) ? &mv : &mk, 64 * c, h,
+                      row0 + (i >> 1) * 128, landed(i));
+      }
+      // nothing leaves the CTA with a copy in flight, whatever the others met
+      mbar_wait(&m->q_full, 0, a.wait_ns, a.err);
+      for (int k = max(0, i - ST); k < i; ++k)
+        mbar_wait(landed(k), landed(k) == &m->full[k % ST] ? (k / ST) & 1 : 0, a.wait_ns, a.err);
+    }
+  } else if (warp == 9) {
+    if (lane == 0) {
+      bool ok = mbar_wait(&m->q_full, 0, a.wait_ns, a.err);
+      ok = ok && mbar_wait(&m->full[0], 0, a.wait_ns, a.err);
+      if (ok) {
+        for (int t = 0; t < 2; ++t)
+          if (n_t[t] > 0) {
+            issue_scores<T, D>(tmem + 128 * t, base + t * C::kHead, ring);
+            tc_commit(&m->s_full[t]);
+          }
+        tc_commit(&m->empty[0]);
+      }
+      for (int j = 0; ok && j < n; ++j) {
+        const int vi = 2 * j + 1, ki = 2 * j + 2;
+        ok = j >= edge ? mbar_wait(&m->clean[j - edge], 0, a.wait_ns, a.err)
+                       : mbar_wait(&m->full[vi % ST], (vi / ST) & 1, a.wait_ns, a.err);
+        if (ok && j + 1 < n) ok = mbar_wait(&m->full[ki % ST], (ki / ST) & 1, a.wait_ns, a.err);
+        for (int t = 0; ok && t < 2; ++t) {
+          if (j >= n_t[t]) continue;
+          ok = mbar_wait(&m->p_full[t], j & 1, a.wait_ns, a.err);
+          if (!ok) break;
+          tc_fence_after();
+          issue_values<T, D>(tmem + 256 + D * t, tmem + 128 * t, ring + (vi % ST) * C::kHead, j > 0);
+          if (j + 1 < n_t[t]) {
+            issue_scores<T, D>(tmem + 128 * t, base + t * C::kHead, ring + (ki % ST) * C::kHead);
+            tc_commit(&m->s_full[t]);
+          } else {
+            tc_commit(&m->o_full[t]);
+          }
+        }
+        if (ok) {
+          tc_commit(&m->empty[vi % ST]);
+          if (j + 1 < n) tc_commit(&m->empty[ki % ST]);
+        }
+      }
+      if (!ok) {  // a wait ran out: the products in flight still end before the memory is given back
+        tc_commit(&m->clean[kEdges - 1]);
+        mbar_wait(&m->clean[kEdges - 1], 0, a.wait_ns, a.err);
+      }
+    }
+  } else if (warp == 10) {
+    for (int j = edge; j < n; ++j) {
+      const int vi = 2 * j + 1;
+      const bool ok = mbar_wait(&m->loaded[j - edge], 0, a.wait_ns, a.err);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      constexpr int CH = D / 8;  // 16-byte chunks of a row
+      const int c = lane % CH;
+      for (int r = lane / CH; r < 128; r += 32 / CH) {
+        uint8_t* at = gbase + C::kRing + (vi % ST) * C::kHead + (c / 8) * kTileBytes + sw128(r, c % 8);
+        const int key = 128 * j + r;
+        if (key >= len) {
+          *reinterpret_cast<uint4*>(at) = make_uint4(0, 0, 0, 0);
+          continue;
+        }
+        const uint4 v = *reinterpret_cast<const uint4*>(at);
+        constexpr uint32_t A = 0x7fff7fffu, B = Elem<T>::kToTop, S = 0x80008000u;
+        if ((((v.x & A) + B) | ((v.y & A) + B) | ((v.z & A) + B) | ((v.w & A) + B)) & S) {
+          uint16_t* e = reinterpret_cast<uint16_t*>(at);
+          for (int i = 0; i < 8; ++i) {
+            const uint32_t x = e[i] & 0x7fffu;
+            if (x < Elem<T>::kInf) continue;
+            atomicMin(&m->first[x > Elem<T>::kInf ? 2 : e[i] >> 15][8 * c + i], key);
+            e[i] = 0;
+            *reinterpret_cast<volatile int*>(&m->dirty) = 1;
+          }
+        }
+      }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&m->clean[j - edge]);
     }
   }
-  T* op = static_cast<T*>(a.out) + row * a.out_stride + qh * D + lane * 2 * W;
-#pragma unroll
-  for (int i = 0; i < 2 * W; ++i) op[i] = static_cast<T>(o[i] / l);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 9) tmem_dealloc(tmem, 512);
+}
+
+template <typename T, int D>
+kvq_status run(const PromptArgs& p, cudaStream_t st, const LaunchCtx& ctx) {
+  using C = Cfg<D>;
+  KernelArgs a{};
+  a.p = p;
+  a.g = p.q_heads / p.heads;
+  a.T = 128 / a.g;
+  a.err = ctx.err;
+  a.wait_ns = ctx.wait_ns;
+  a.mul = p.scale * 1.4426950408889634f;
+  const CUtensorMapDataType type = p.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  CUtensorMap mq, mk, mv;
+  auto map = [&](CUtensorMap* m, const void* x, int heads, int64_t stride, uint32_t bh, uint32_t br) {
+    const uint64_t dims[3] = {D, static_cast<uint64_t>(heads), static_cast<uint64_t>(p.n_rows)};
+    const uint64_t str[2] = {2 * D, static_cast<uint64_t>(stride) * 2};
+    const uint32_t box[3] = {64, bh, br};
+    return make_map(m, type, 3, x, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B);
+  };
+  if (!map(&mq, p.q, p.q_heads, p.q_stride, static_cast<uint32_t>(a.g), static_cast<uint32_t>(a.T)) ||
+      !map(&mk, p.k, p.heads, p.k_stride, 1, 128) || !map(&mv, p.v, p.heads, p.v_stride, 1, 128))
+    return KVQ_ERR_CUDA;
+  const long long TT = 2 * a.T;
+  const long long by_rows = p.n_rows / TT + p.n_seqs, by_max = p.n_seqs * ((p.max_rows + TT - 1) / TT);
+  const long long grid = (by_rows < by_max ? by_rows : by_max) * p.heads;
+  if (grid >= (1ll << 31)) return KVQ_ERR_UNSUPPORTED;
+  if (!set_smem_once(reinterpret_cast<const void*>(k_prompt_tiles<T, D>), C::kSmem)) return KVQ_ERR_CUDA;
+  k_prompt_tiles<T, D><<<static_cast<unsigned>(grid), kThreads, C::kSmem, st>>>(a, mq, mk, mv);
+  return launch_status();
 }
 
 }  // namespace
 
-kvq_status launch_attend_prompt(const PromptArgs& p, cudaStream_t st, const LaunchCtx&) {
-  const unsigned grid = static_cast<unsigned>((static_cast<long long>(p.n_rows) * p.q_heads + 7) / 8);
-  if (p.bf16) {
-    if (p.head_dim == 128) k_prompt_rows<__nv_bfloat16, 128><<<grid, 256, 0, st>>>(p);
-    else k_prompt_rows<__nv_bfloat16, 64><<<grid, 256, 0, st>>>(p);
-  } else {
-    if (p.head_dim == 128) k_prompt_rows<__half, 128><<<grid, 256, 0, st>>>(p);
-    else k_prompt_rows<__half, 64><<<grid, 256, 0, st>>>(p);
-  }
-  return launch_status();
+kvq_status launch_attend_prompt(const PromptArgs& p, cudaStream_t st, const LaunchCtx& ctx) {
+  if (p.bf16) return p.head_dim == 128 ? run<__nv_bfloat16, 128>(p, st, ctx) : run<__nv_bfloat16, 64>(p, st, ctx);
+  return p.head_dim == 128 ? run<__half, 128>(p, st, ctx) : run<__half, 64>(p, st, ctx);
 }
 
 }  // namespace kvq
