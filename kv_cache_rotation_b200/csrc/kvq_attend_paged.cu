@@ -1,19 +1,37 @@
 // Attention of packed new rows over the pages of a compressed cache
 // (kvq_attend_paged). With y the dequantized record and R = P^T H the rotation
-// of a head, khat = R y and vhat = R y, so
+// of a head (an orthonormal map), khat = R y and vhat = R y, so
 //   q . khat = (R^T q) . y,   sum_n p_n vhat_n = R (sum_n p_n y_n):
-// the query is rotated once, the output once. The sinks' fp16 rows enter in
-// their own basis.
+// the query is rotated once, the output once, and the records are only
+// dequantized. The sinks' fp16 rows enter in their own basis, in fp32.
+//
+// k_paged_tiles: a CTA takes a tile of query rows of one KV head (row t * g +
+// j is token t, query head j of the group of g) and a stretch of its keys, in
+// tiles of 128. Eight warps turn records into fp16 tiles in shared memory (read
+// through the block table, a thread per half record), one thread issues the
+// products, and a warpgroup per slot does the softmax (kvq_flash.cuh). The two
+// slots are two tiles of 128 rows that share every tile of keys (a chunk of a
+// prompt: SHARED), or the same rows with alternate tiles of keys (up to 128 rows,
+// a decode step: the second slot is then half of the stretch). Each slot leaves
+// its sums, reference and weight total per row in the workspace.
+// k_paged_merge: one warp per row and query head joins them with the sinks and
+// turns the result back.
 #include <math.h>
 
-#include "kvq_device.cuh"
+#include "kvq_flash.cuh"
 #include "kvq_internal.h"
 
 namespace kvq {
 namespace {
 
+constexpr int kProdWarps = 8;
+constexpr int kThreads = 32 * (8 + kProdWarps + 1);  // softmax 0-7, records 8-15, products 16
+constexpr int kMasks = 8;  // key masks kept: more tiles than are in flight
+
 struct PagedArgs {
-  int S, n_rows, max_pages, sink_rows, H, Hq, g, ps, n_pages, n_sink, rope, rope_rows, rot, group, max_rows;
+  int S, n_rows, max_pages, sink_rows, H, Hq, g, T, n_pages, n_sink, rope, rope_rows, rot, max_rows;
+  int stretch, n_stretch, n_parts;  // keys of a CTA, CTAs along the keys, partial results per row
+  FastDiv div_ps;
   int64_t q_stride, out_stride;
   float scale, rscale;
   const __half* q;
@@ -24,9 +42,175 @@ struct PagedArgs {
   const uint8_t *kcodes, *vcodes;
   const __half2 *ksz, *vsz;
   const __half *ksink, *vsink;
+  float* part_o;   // [n_parts][n_rows * Hq][D], channels in tile order
+  float2* part_s;  // [n_parts][n_rows * Hq] (reference in log2, weight total)
+  uint32_t* err;
+  uint64_t wait_ns;
 };
 
-// FWHT of D channels, D / 32 consecutive ones per lane, unnormalised.
+// Channels sit in the tiles in the order that the codes unpack to: the two codes
+// of a 32-bit register of halves come from the same bit of its two halves.
+template <int BITS>
+__host__ __device__ constexpr int tile_pos(int ch) {
+  if (BITS == 2) return (ch & ~15) + 2 * (ch & 7) + ((ch >> 3) & 1);
+  if (BITS == 4) return (ch & ~7) + 2 * (ch & 3) + ((ch >> 2) & 1);
+  const int u = ch & 31;  // 3 bits: three runs of 10 codes, then two
+  return u >= 30 ? ch : (ch & ~31) + 2 * (5 * (u / 10) + u % 5) + (u % 10) / 5;
+}
+
+// 2^-p as an fp16 pair, and -1024 * 2^-p.
+__host__ __device__ constexpr uint32_t h2_exp(int p) { return static_cast<uint32_t>(15 - p) * 0x04000400u; }
+__host__ __device__ constexpr uint32_t h2_bias(int p) { return 0x80008000u + static_cast<uint32_t>(25 - p) * 0x04000400u; }
+__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+// The codes of BITS bits at bit `p` of both halves of x as y = c S + Z: 1024 + c 2^p is put together
+// by masking, made c exactly by one fma, and rounded once to fp16 by the next.
+template <int BITS, int P>
+__device__ __forceinline__ uint32_t code_pair(uint32_t x, uint32_t S, uint32_t Z) {
+  static_assert(P + BITS <= 10, "inside the mantissa");
+  constexpr uint32_t M = ((1u << BITS) - 1u) << P;
+  const uint32_t v = (x & (M | (M << 16))) | 0x64006400u;
+  return hfma2(hfma2(v, h2_exp(P), h2_bias(P)), S, Z);
+}
+
+// One unit of codes (2 bits: a word, 16 channels; 4 bits: a word, 8; 3 bits: three words, 32) as
+// fp16 pairs in tile order.
+template <int BITS>
+struct Unit;
+template <>
+struct Unit<2> {
+  static constexpr int kWords = 1, kPairs = 8;
+  static __device__ __forceinline__ void open(const uint32_t* w, uint32_t S, uint32_t Z, uint32_t* o) {
+    const uint32_t a = w[0], b = w[0] >> 10;
+    o[0] = code_pair<2, 0>(a, S, Z);
+    o[1] = code_pair<2, 2>(a, S, Z);
+    o[2] = code_pair<2, 4>(a, S, Z);
+    o[3] = code_pair<2, 6>(a, S, Z);
+    o[4] = code_pair<2, 8>(a, S, Z);
+    o[5] = code_pair<2, 0>(b, S, Z);
+    o[6] = code_pair<2, 2>(b, S, Z);
+    o[7] = code_pair<2, 4>(b, S, Z);
+  }
+};
+template <>
+struct Unit<4> {
+  static constexpr int kWords = 1, kPairs = 4;
+  static __device__ __forceinline__ void open(const uint32_t* w, uint32_t S, uint32_t Z, uint32_t* o) {
+    const uint32_t a = w[0], b = w[0] >> 8;
+    o[0] = code_pair<4, 0>(a, S, Z);
+    o[1] = code_pair<4, 4>(a, S, Z);
+    o[2] = code_pair<4, 0>(b, S, Z);
+    o[3] = code_pair<4, 4>(b, S, Z);
+  }
+};
+template <>
+struct Unit<3> {
+  static constexpr int kWords = 3, kPairs = 16;
+  static __device__ __forceinline__ void open(const uint32_t* w, uint32_t S, uint32_t Z, uint32_t* o) {
+    const uint32_t run[3] = {w[0], __funnelshift_r(w[0], w[1], 30), __funnelshift_r(w[1], w[2], 28)};
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {  // codes 0-4 in the low half, 5-9 in the high half
+      const uint32_t a = (run[k] & 0x7fffu) | ((run[k] << 1) & 0x7fff0000u), b = a >> 9;
+      o[5 * k] = code_pair<3, 0>(a, S, Z);
+      o[5 * k + 1] = code_pair<3, 3>(a, S, Z);
+      o[5 * k + 2] = code_pair<3, 6>(a, S, Z);
+      o[5 * k + 3] = code_pair<3, 0>(b, S, Z);
+      o[5 * k + 4] = code_pair<3, 3>(b, S, Z);
+    }
+    const uint32_t a = ((w[2] >> 26) & 7u) | ((w[2] >> 13) & 0x70000u);
+    o[15] = code_pair<3, 0>(a, S, Z);
+  }
+};
+
+// Half a record in registers.
+template <int D, int BITS, int G>
+struct Half {
+  static constexpr int kCh = D / 2, kWords = kCh * BITS / 32, kSz = G >= kCh ? 1 : kCh / G;
+  uint32_t w[kWords], sz[kSz];
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = 0;
+#pragma unroll
+    for (int i = 0; i < kSz; ++i) sz[i] = 0;
+  }
+  __device__ __forceinline__ void load(const uint8_t* codes, const __half2* s, size_t rec, int half) {
+    const uint8_t* p = codes + rec * (D * BITS / 8) + half * (4 * kWords);
+    if constexpr (kWords % 4 == 0) {
+#pragma unroll
+      for (int i = 0; i < kWords / 4; ++i) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + i);
+        w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+      }
+    } else if constexpr (kWords % 2 == 0) {
+#pragma unroll
+      for (int i = 0; i < kWords / 2; ++i) {
+        const uint2 v = __ldg(reinterpret_cast<const uint2*>(p) + i);
+        w[2 * i] = v.x, w[2 * i + 1] = v.y;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) w[i] = __ldg(reinterpret_cast<const uint32_t*>(p) + i);
+    }
+    const uint32_t* z = reinterpret_cast<const uint32_t*>(s) + rec * (D / G) + (G >= D ? 0 : half * kSz);
+#pragma unroll
+    for (int i = 0; i < kSz; ++i) sz[i] = __ldg(z + i);
+  }
+  // Row r of a tile: this half's channels as fp16. The two halves of a record write the 16-byte
+  // chunks in an order four apart, so the 8 lanes of a store phase meet 8 different bank groups.
+  __device__ __forceinline__ void store(uint32_t tile, int r, int half) const {
+    using U = Unit<BITS>;
+    constexpr int UC = 2 * U::kPairs;  // channels of a unit
+    constexpr int UW = U::kWords;
+    constexpr int NU = kCh / UC;
+    constexpr int TB = D == 128 ? 1 : 0;  // D = 64: both halves in one 128-byte row
+    const uint32_t row = tile + (TB ? half * kTileBytes : 0) + r * 128u;
+    const int x = (r & 7) ^ (TB ? half * 4 : 0);
+#pragma unroll
+    for (int u = 0; u < NU; ++u) {
+      // the unit that goes to the chunks of u, with the halves' order swapped
+      uint32_t in[UW];
+      constexpr int SW = NU >= 2 && TB ? NU / 2 : 0;
+#pragma unroll
+      for (int i = 0; i < UW; ++i) in[i] = SW ? (half ? w[((u + SW) % NU) * UW + i] : w[u * UW + i]) : w[u * UW + i];
+      const uint32_t sa = sz[kSz == 1 ? 0 : u * UC / G], sb = sz[kSz == 1 ? 0 : ((u + SW) % NU) * UC / G];
+      const uint32_t s = SW && half ? sb : sa;
+      const uint32_t S = __byte_perm(s, s, 0x1010), Z = __byte_perm(s, s, 0x3232);
+      uint32_t o[U::kPairs];
+      U::open(in, S, Z, o);
+#pragma unroll
+      for (int c = 0; c < UC / 8; ++c) {
+        const int chunk = u * (UC / 8) + c;  // before the swap; D = 64: the half's own four chunks
+        const uint32_t at = TB ? static_cast<uint32_t>((chunk ^ x) << 4)
+                               : static_cast<uint32_t>(((chunk + half * 4) ^ (r & 7)) << 4);
+        sts128(row + at, make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]));
+      }
+    }
+  }
+};
+
+template <int D, bool SHARED>
+struct Cfg {
+  static constexpr uint32_t kHead = D / 64 * kTileBytes;
+  static constexpr uint32_t kK = (SHARED ? 2 : 1) * kHead;  // two stages of keys behind the query rows
+  static constexpr uint32_t kV = kK + 2 * kHead;
+  static constexpr uint32_t kMisc = kV + 2 * kHead;
+  static constexpr uint32_t kSmem = kMisc + 2048 + 1024;
+  static constexpr int kAhead = SHARED ? 1 : 2;  // tiles of keys before the first tile of values
+};
+
+struct Misc {
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full[2], drain;
+  uint32_t tmem;
+  RowItem item;
+  uint32_t seen[kMasks][4];
+  float mul[2][128];
+};
+static_assert(sizeof(Misc) <= 2048, "fits behind the rings");
+
+// FWHT of D channels, C = D / 32 consecutive ones per lane, unnormalised.
 template <int C>
 __device__ __forceinline__ void warp_fwht(float (&x)[C], int lane) {
   fwht_reg<C>(x);
@@ -43,89 +227,377 @@ __device__ __forceinline__ float all_sum(float v) {
   for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
-
-// This lane's C codes of a record, dequantized.
-template <int C, int BITS>
-__device__ __forceinline__ void read_record(const uint8_t* rec, const __half2* sz, int group, int lane, float (&y)[C]) {
-  const int bit = lane * C * BITS;
-  const float2 p = __half22float2(sz[lane * C / group]);
+__device__ __forceinline__ float all_max(float v) {
 #pragma unroll
-  for (int i = 0; i < C; ++i) {
-    const int b = bit + i * BITS;
-    uint32_t c = rec[b >> 3] >> (b & 7);
-    if ((b & 7) + BITS > 8) c |= static_cast<uint32_t>(rec[(b >> 3) + 1]) << (8 - (b & 7));
-    y[i] = fmaf(static_cast<float>(c & ((1u << BITS) - 1u)), p.x, p.y);
-  }
+  for (int o = 16; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
 }
 
-// One warp per (row, query head).
+// Positions that a block_table row covers.
+__device__ __forceinline__ int sat_pages(int pages, int ps) {
+  const long long v = static_cast<long long>(pages) * ps;
+  return v > 0x7fffffffll ? 0x7fffffff : static_cast<int>(v);
+}
+
+template <int D, int BITS, int G, bool SHARED>
+__global__ void __launch_bounds__(kThreads, 1) k_paged_tiles(const PagedArgs a) {
+  using C = Cfg<D, SHARED>;
+  extern __shared__ uint8_t flash_smem[];
+  const uint32_t base = (smem_u32(flash_smem) + 1023u) & ~1023u;
+  uint8_t* const gbase = flash_smem + (base - smem_u32(flash_smem));
+  Misc* const m = reinterpret_cast<Misc*>(gbase + C::kMisc);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // blocks in the order: key stretch, KV head, row tile (fastest to slowest)
+  unsigned rest = blockIdx.x;
+  const int z = static_cast<int>(rest % static_cast<unsigned>(a.n_stretch));
+  rest /= static_cast<unsigned>(a.n_stretch);
+  const int h = static_cast<int>(rest % static_cast<unsigned>(a.H));
+  const int idx = static_cast<int>(rest / static_cast<unsigned>(a.H));
+  constexpr int SLOTS = SHARED ? 2 : 1;  // tiles of query rows
+
+  // the merge kernel may start once every CTA has: its prologue reads inputs alone
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (warp == 16) find_item(a.cu_rows, a.S, a.n_rows, a.max_rows, SLOTS * a.T, idx, lane, &m->item);
+  __syncthreads();
+  const RowItem it = m->item;
+  if (it.len == 0) return;
+  const int cached = max(__ldg(a.kv_len + it.seq), 0);
+  const int kv = min(cached, sat_pages(a.max_pages, static_cast<int>(a.div_ps.d)));
+  const int pos0 = cached - it.rows + it.q0;  // position of the tile's first token
+  const int tokens = min(it.len - it.q0, SLOTS * a.T);
+  // keys [k0, k1): this stretch, cut at what the last token sees; the last stretch has no end
+  const long long kb = static_cast<long long>(z) * a.stretch;
+  const long long ke = z + 1 == a.n_stretch ? 0x7fffffffll : kb + a.stretch;
+  const int k0 = static_cast<int>(min(kb, 0x7fffffffll));
+  const int k1 = static_cast<int>(min(ke, static_cast<long long>(min(kv, pos0 + tokens))));
+  if (k1 <= k0) return;  // no row of the tile sees a key here: the merge does not look
+  const int n = (k1 - k0 + 127) >> 7;
+
+  if (warp == 16) tmem_alloc(&m->tmem, 512);
+  const int live_warps = min(4, (min(tokens, a.T) * a.g + 31) >> 5);  // of a slot, with rows of a token
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&m->k_full[i], kProdWarps), mbar_init(&m->v_full[i], kProdWarps);
+      mbar_init(&m->k_empty[i], 1), mbar_init(&m->v_empty[i], 1);
+      mbar_init(&m->s_full[i], 1), mbar_init(&m->o_full[i], 1);
+      mbar_init(&m->p_full[i], SHARED ? 4 : live_warps);
+    }
+    mbar_init(&m->drain, 1);
+    fence_mbar_init();
+  }
+  // the query rows, rotated, scaled by a power of two into [1, 2) and rounded once to fp16
+  {
+    constexpr int CH = D / 32;
+    for (int r = warp; r < tokens * a.g; r += kThreads / 32) {
+      const int tok = r / a.g, j = r - tok * a.g, t = tok / a.T, tr = r - t * a.T * a.g;
+      const __half* qp = a.q + (static_cast<int64_t>(it.row0) + it.q0 + tok) * a.q_stride + (h * a.g + j) * D;
+      float x[CH];
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        const int ch = lane * CH + c;
+        x[c] = __half2float(qp[a.kperm ? a.kperm[h * D + ch] & (D - 1) : ch]);
+      }
+      if (a.rot) {
+        warp_fwht<CH>(x, lane);
+#pragma unroll
+        for (int c = 0; c < CH; ++c) x[c] *= a.rscale;
+      }
+      float top = 0.0f;
+#pragma unroll
+      for (int c = 0; c < CH; ++c) top = fmaxf(top, fabsf(x[c]));
+      top = all_max(top);
+      const int e = top > 0.0f && top < INFINITY ? static_cast<int>(__float_as_uint(top) >> 23) - 127 : 0;
+      const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        const int p = tile_pos<BITS>(lane * CH + c);
+        *reinterpret_cast<__half*>(gbase + t * C::kHead + (p / 64) * kTileBytes + sw128(tr, (p % 64) / 8) + 2 * (p % 8)) =
+            __float2half_rn(x[c] * down);
+      }
+      if (lane == 0) m->mul[t][tr] = a.scale * 1.4426950408889634f * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+    }
+    fence_async_smem();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = m->tmem;
+  // tiles of keys of each slot
+  int n_t[2];
+  if (SHARED) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const int last = min(k1, pos0 + min(tokens, (t + 1) * a.T));
+      n_t[t] = tokens > t * a.T && last > k0 ? (last - k0 + 127) >> 7 : 0;
+    }
+  } else {
+    n_t[0] = (n + 1) >> 1;
+    n_t[1] = n >> 1;
+  }
+
+  if (warp < 8) {
+    const int t = warp >> 2, tq = SHARED ? t : 0;
+    const int r = tid & 127, tok = tq * a.T + r / a.g, j = r % a.g;
+    const bool mine = r < a.T * a.g && tok < tokens;
+    const int lim = mine ? pos0 + tok + 1 : 0x7fffffff;
+    const float mul = mine ? m->mul[tq][r] : 0.0f;
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>(warp & 3) << 21);
+    const uint32_t s_addr = lane_base + 128 * t, o_addr = lane_base + 256 + D * t;
+    RowStat st;
+    bool ok = true;
+    const bool works = SHARED || (warp & 3) < live_warps;
+    const int nt = works ? n_t[t] : 0;
+    for (int i = 0; i < nt; ++i) {
+      ok = __all_sync(0xffffffffu, mbar_wait(&m->s_full[t], i & 1, a.wait_ns, a.err));
+      if (!ok) break;
+      tc_fence_after();
+      const int tile = SHARED ? i : 2 * i + t;
+      const uint4 bits = *reinterpret_cast<const uint4*>(m->seen[tile % kMasks]);
+      const int left = lim - (k0 + 128 * tile);
+      const bool whole = left >= 128 && (bits.x & bits.y & bits.z & bits.w) == 0xffffffffu;
+      const uint32_t seen[4] = {bits.x & first_bits(left, 0), bits.y & first_bits(left, 32),
+                                bits.z & first_bits(left, 64), bits.w & first_bits(left, 96)};
+      if (__all_sync(0xffffffffu, whole))
+        softmax_tile<__half, D, false, false>(s_addr, o_addr, i > 0, mul, st, seen);
+      else
+        softmax_tile<__half, D, true, false>(s_addr, o_addr, i > 0, mul, st, seen);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&m->p_full[t]);
+    }
+    if (ok && nt > 0) ok = __all_sync(0xffffffffu, mbar_wait(&m->o_full[t], 0, a.wait_ns, a.err));
+    if (ok && works) {
+      const size_t at = static_cast<size_t>(SHARED ? z : 2 * z + t) * (static_cast<size_t>(a.n_rows) * a.Hq) +
+                        (static_cast<size_t>(it.row0) + it.q0 + tok) * a.Hq + h * a.g + j;
+      if (mine) a.part_s[at] = make_float2(st.m, st.l);
+      if (nt > 0) {
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          tmem_ld32(o_addr + 32 * c, o);
+          tmem_wait_ld32(o);
+          if (mine) {
+            uint4* dst = reinterpret_cast<uint4*>(a.part_o + at * D + 32 * c);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) dst[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          }
+        }
+      }
+    }
+  } else if (warp < 16) {
+    const int p = tid - 256, r = p >> 1, half = p & 1;
+    using R = Half<D, BITS, G>;
+    const int32_t* table = a.block_table + static_cast<size_t>(it.seq) * a.max_pages;
+    // page of this thread's key of tile i; -1 outside the stretch, among the sinks, behind the last tile
+    auto page_of = [&](int i) {
+      if (i >= n) return -1;
+      const int pos = k0 + 128 * i + r;
+      if (pos >= k1 || pos < a.n_sink) return -1;
+      const int pg = __ldg(table + a.div_ps.div(static_cast<uint32_t>(pos)));
+      return pg < a.n_pages ? pg : -1;
+    };
+    auto fetch = [&](int i, int pg, R& k, R& v) {
+      if (pg < 0) {
+        k.clear();
+        v.clear();
+        return;
+      }
+      const uint32_t pos = static_cast<uint32_t>(k0 + 128 * i + r);
+      const size_t rec = (static_cast<size_t>(pg) * a.H + h) * a.div_ps.d + a.div_ps.mod(pos, a.div_ps.div(pos));
+      k.load(a.kcodes, a.ksz, rec, half);
+      v.load(a.vcodes, a.vsz, rec, half);
+    };
+    bool ok = true;
+    auto put = [&](int i, const R& x, uint64_t* full, uint64_t* empty, uint32_t ring) {
+      const int s = i & 1;
+      if (i >= 2) ok = ok && mbar_wait(&empty[s], ((i >> 1) & 1) ^ 1, a.wait_ns, a.err);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) return;
+      x.store(base + ring + s * C::kHead, r, half);
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&full[s]);
+    };
+    // records two tiles ahead in registers, their pages three; K_i goes in before V_(i + 1 - kAhead)
+    R kr[2], vr[2], vlate;
+    int pg[2] = {page_of(0), page_of(1)}, pn = page_of(2);
+    fetch(0, pg[0], kr[0], vr[0]);
+    fetch(1, pg[1], kr[1], vr[1]);
+    for (int i0 = 0; ok && i0 < n + C::kAhead - 1; i0 += 2) {
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const int i = i0 + b;
+        if (i < n) {
+          const uint32_t seen = __ballot_sync(0xffffffffu, pg[b] >= 0);
+          if (lane == 0) {  // two lanes a key
+            uint32_t x = seen & 0x55555555u;
+            x = (x | (x >> 1)) & 0x33333333u;
+            x = (x | (x >> 2)) & 0x0f0f0f0fu;
+            x = (x | (x >> 4)) & 0x00ff00ffu;
+            x = (x | (x >> 8)) & 0x0000ffffu;
+            reinterpret_cast<uint16_t*>(m->seen[i % kMasks])[warp - 8] = static_cast<uint16_t>(x);
+          }
+          put(i, kr[b], m->k_full, m->k_empty, C::kK);
+        }
+        const int j = i + 1 - C::kAhead;
+        if (j >= 0 && j < n) put(j, C::kAhead == 1 ? vr[b] : vlate, m->v_full, m->v_empty, C::kV);
+        if (!ok) break;
+        if (C::kAhead == 2) vlate = vr[b];
+        pg[b] = pn;
+        fetch(i + 2, pg[b], kr[b], vr[b]);
+        pn = page_of(i + 3);
+      }
+    }
+  } else {
+    if (lane == 0) {
+      bool ok = true;
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        ok = ok && mbar_wait(bar, parity, a.wait_ns, a.err);
+        return ok;
+      };
+      auto scores = [&](int t, int j) {
+        issue_scores<__half, D>(tmem + 128 * t, base + (SHARED ? t : 0) * C::kHead, base + C::kK + (j & 1) * C::kHead);
+        tc_commit(&m->s_full[t]);
+      };
+      auto values = [&](int t, int j, bool acc) {
+        issue_values<__half, D>(tmem + 256 + D * t, tmem + 128 * t, base + C::kV + (j & 1) * C::kHead, acc);
+      };
+      if (SHARED) {
+        if (wait(&m->k_full[0], 0)) {
+          for (int t = 0; t < 2; ++t)
+            if (n_t[t] > 0) scores(t, 0);
+          tc_commit(&m->k_empty[0]);
+        }
+        for (int j = 0; ok && j < n; ++j) {
+          wait(&m->v_full[j & 1], (j >> 1) & 1);
+          if (j + 1 < n) wait(&m->k_full[(j + 1) & 1], ((j + 1) >> 1) & 1);
+          for (int t = 0; ok && t < 2; ++t) {
+            if (j >= n_t[t] || !wait(&m->p_full[t], j & 1)) continue;
+            tc_fence_after();
+            values(t, j, j > 0);
+            if (j + 1 < n_t[t]) scores(t, j + 1);
+            else tc_commit(&m->o_full[t]);
+          }
+          if (!ok) break;
+          tc_commit(&m->v_empty[j & 1]);
+          if (j + 1 < n) tc_commit(&m->k_empty[(j + 1) & 1]);
+        }
+      } else {
+        for (int j = 0; j < 2 && j < n; ++j)
+          if (wait(&m->k_full[j], 0)) {
+            scores(j, j);
+            tc_commit(&m->k_empty[j]);
+          }
+        for (int j = 0; ok && j < n; ++j) {
+          const int t = j & 1;
+          wait(&m->v_full[t], (j >> 1) & 1);
+          if (j + 2 < n) wait(&m->k_full[t], ((j + 2) >> 1) & 1);
+          if (!wait(&m->p_full[t], (j >> 1) & 1)) break;
+          tc_fence_after();
+          values(t, j, j > 1);
+          tc_commit(&m->v_empty[t]);
+          if (j + 2 < n) {
+            scores(t, j + 2);
+            tc_commit(&m->k_empty[t]);
+          } else {
+            tc_commit(&m->o_full[t]);
+          }
+        }
+      }
+      if (!ok) {  // a wait ran out: the products in flight still end before the memory is given back
+        tc_commit(&m->drain);
+        mbar_wait(&m->drain, 0, a.wait_ns, a.err);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 16) tmem_dealloc(tmem, 512);
+}
+
+// One warp per row and query head, C = D / 32 channels a lane.
 template <int D, int BITS>
-__global__ void __launch_bounds__(128) k_paged_rows(const PagedArgs a) {
-  constexpr int C = D / 32, RB = D * BITS / 8;
-  __shared__ float nat[4][D];
+__global__ void __launch_bounds__(256) k_paged_merge(const PagedArgs a) {
+  constexpr int C = D / 32;
+  __shared__ float nat[8][D];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const long long wi = blockIdx.x * 4ll + warp;
+  const long long wi = blockIdx.x * 8ll + warp;
   const int row = static_cast<int>(wi / a.Hq), qh = static_cast<int>(wi % a.Hq);
   if (row >= a.n_rows) return;
-  int seq = -1, m = 0, i = 0;
-  for (int s = 0; s < a.S; ++s) {
-    const int b = __ldg(a.cu_rows + s), e = min(a.n_rows, __ldg(a.cu_rows + s + 1));
-    if (row >= b && row < e && row - b < a.max_rows) seq = s, m = e - b, i = row - b;
+  // the sequence whose rows hold this one
+  int lo = 0, hi = a.S;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (__ldg(a.cu_rows + mid) <= row) lo = mid; else hi = mid;
   }
-  if (seq < 0) return;
-  const int h = qh / a.g, last = __ldg(a.kv_len + seq) - m + i;  // the last visible position
-  const __half* qp = a.q + row * a.q_stride + qh * D;
-  float q[C], qr[C], o[C], on[C], mx = -INFINITY, l = 0.0f;
+  const int b = min(max(__ldg(a.cu_rows + lo), 0), a.n_rows), e = min(max(__ldg(a.cu_rows + lo + 1), b), a.n_rows);
+  if (row < b || row >= e || row - b >= a.max_rows) return;
+  const int h = qh / a.g, len = max(__ldg(a.kv_len + lo), 0);
+  // keys [0, lim)
+  const int lim = min(len - (e - b) + (row - b) + 1, min(len, sat_pages(a.max_pages, static_cast<int>(a.div_ps.d))));
+  const float unit = a.scale * 1.4426950408889634f;
+  float top = -INFINITY, total = 0.0f, own[C];
 #pragma unroll
-  for (int c = 0; c < C; ++c) {
-    q[c] = __half2float(qp[lane * C + c]);
-    qr[c] = a.kperm ? __half2float(qp[a.kperm[h * D + lane * C + c] & (D - 1)]) : q[c];
-    o[c] = on[c] = 0.0f;
-  }
-  if (a.rot) {
-    warp_fwht<C>(qr, lane);
+  for (int c = 0; c < C; ++c) own[c] = 0.0f;
+  if (a.n_sink > 0) {  // the sinks' running sums, in their own basis
+    const int srow = a.sink_slot ? __ldg(a.sink_slot + lo) : lo;
+    const __half* qp = a.q + row * a.q_stride + qh * D + lane * C;
+    float q[C];
 #pragma unroll
-    for (int c = 0; c < C; ++c) qr[c] *= a.rscale;
-  }
-  const int srow = a.n_sink ? (a.sink_slot ? __ldg(a.sink_slot + seq) : seq) : -1;
-  for (int n = 0; n <= last; ++n) {
-    float k[C], v[C], s = 0.0f;
-    const bool sink = n < a.n_sink;
-    const int pg = n / a.ps < a.max_pages ? __ldg(a.block_table + static_cast<size_t>(seq) * a.max_pages + n / a.ps) : -1;
-    if (pg < 0 || pg >= a.n_pages) continue;
-    if (sink) {
-      if (srow < 0 || srow >= a.sink_rows || (a.rope && n >= a.rope_rows)) continue;
+    for (int c = 0; c < C; ++c) q[c] = __half2float(qp[c]);
+    const int last = srow >= 0 && srow < a.sink_rows ? min(a.n_sink, lim) : 0;
+    for (int n = 0; n < last; ++n) {
+      const int pg = __ldg(a.block_table + static_cast<size_t>(lo) * a.max_pages + a.div_ps.div(static_cast<uint32_t>(n)));
+      if (pg < 0 || pg >= a.n_pages || (a.rope && n >= a.rope_rows)) continue;
       const size_t at = ((static_cast<size_t>(srow) * a.H + h) * a.n_sink + n) * D;
+      float s = 0.0f;
 #pragma unroll
       for (int c = 0; c < C; ++c) {
         const int j = lane * C + c;
         float x = __half2float(a.ksink[at + j]);
         if (a.rope) {
-          const int j2 = a.rope == 1 ? j ^ 1 : (j < D / 2 ? j + D / 2 : j - D / 2), pr = a.rope == 1 ? j / 2 : j % (D / 2);
+          const bool pairs = a.rope == 1;
+          const int j2 = pairs ? j ^ 1 : (j + D / 2) % D, pr = pairs ? j / 2 : j % (D / 2);
           const float2 cs = reinterpret_cast<const float2*>(a.rope_cs)[static_cast<size_t>(n) * (D / 2) + pr];
-          const bool up = a.rope == 1 ? (j & 1) : j >= D / 2;
           const float x2 = __half2float(a.ksink[at + j2]);
-          x = up ? fmaf(x2, cs.y, x * cs.x) : fmaf(x, cs.x, -(x2 * cs.y));
+          x = (pairs ? (j & 1) != 0 : j >= D / 2) ? fmaf(x2, cs.y, x * cs.x) : fmaf(x, cs.x, -(x2 * cs.y));
         }
         s = fmaf(q[c], x, s);
-        v[c] = __half2float(a.vsink[at + j]);
       }
-    } else {
-      const size_t rec = (static_cast<size_t>(pg) * a.H + h) * a.ps + n % a.ps;
-      read_record<C, BITS>(a.kcodes + rec * RB, a.ksz + rec * (D / a.group), a.group, lane, k);
-      read_record<C, BITS>(a.vcodes + rec * RB, a.vsz + rec * (D / a.group), a.group, lane, v);
+      s = all_sum(s) * unit;
+      const float mn = fmaxf(top, s), f = top == mn ? 1.0f : exp2f(top - mn), p = exp2f(s - mn);
+      top = mn;
+      total = fmaf(total, f, p);
 #pragma unroll
-      for (int c = 0; c < C; ++c) s = fmaf(qr[c], k[c], s);
+      for (int c = 0; c < C; ++c) own[c] = own[c] * f + p * __half2float(a.vsink[at + lane * C + c]);
     }
-    s = all_sum(s) * a.scale;
-    const float mn = fmaxf(mx, s), f = mx == mn ? 1.0f : __expf(mx - mn), p = __expf(s - mn);
-    mx = mn;
-    l = fmaf(l, f, p);
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // the stretches that hold keys of this row, an empty one (weight total 0) left out
+  const size_t rows = static_cast<size_t>(a.n_rows) * a.Hq, me = static_cast<size_t>(row) * a.Hq + qh;
+  const int per = a.n_parts / a.n_stretch;
+  const int parts = lim > 0 ? min(a.n_stretch, (lim - 1) / a.stretch + 1) * per : 0;
+  float all_top = top;
+  for (int p0 = 0; p0 < parts; p0 += 32) {
+    const float2 s = p0 + lane < parts ? a.part_s[(p0 + lane) * rows + me] : make_float2(-INFINITY, 0.0f);
+    all_top = fmaxf(all_top, all_max(s.y != 0.0f ? s.x : -INFINITY));
+  }
+  const float ref = all_top == -INFINITY ? 0.0f : all_top;
+  float o[C];
+  const float fs = exp2f(top - ref);
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      o[c] = o[c] * f + (sink ? 0.0f : p * v[c]);
-      on[c] = on[c] * f + (sink ? p * v[c] : 0.0f);
-    }
+  for (int c = 0; c < C; ++c) o[c] = 0.0f, own[c] *= fs;
+  total *= fs;
+  for (int p = 0; p < parts; ++p) {
+    const float2 s = a.part_s[p * rows + me];
+    if (s.y == 0.0f) continue;
+    const float f = exp2f(s.x - ref);
+    total = fmaf(s.y, f, total);
+    const float* src = a.part_o + (p * rows + me) * D;
+#pragma unroll
+    for (int c = 0; c < C; ++c) o[c] = fmaf(src[tile_pos<BITS>(lane * C + c)], f, o[c]);
   }
   if (a.rot) {
     warp_fwht<C>(o, lane);
@@ -135,20 +607,85 @@ __global__ void __launch_bounds__(128) k_paged_rows(const PagedArgs a) {
 #pragma unroll
   for (int c = 0; c < C; ++c) nat[warp][a.vperm ? a.vperm[h * D + lane * C + c] & (D - 1) : lane * C + c] = o[c];
   __syncwarp();
-  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+  const float inv = total != 0.0f ? 1.0f / total : 0.0f;
+  __half* out = a.out + row * a.out_stride + qh * D + lane * C;
 #pragma unroll
-  for (int c = 0; c < C; ++c)
-    a.out[row * a.out_stride + qh * D + lane * C + c] = __float2half_rn((nat[warp][lane * C + c] + on[c]) * inv);
+  for (int c = 0; c < C; c += 2)
+    *reinterpret_cast<__half2*>(out + c) = __floats2half2_rn((nat[warp][lane * C + c] + own[c]) * inv,
+                                                             (nat[warp][lane * C + c + 1] + own[c + 1]) * inv);
 }
+
+// How a call's work is cut: row tiles, and stretches of keys per tile.
+struct Plan {
+  bool shared;
+  int T, stretch, n_stretch, n_parts;
+  long long tiles;
+};
+Plan make_plan(int q_heads, int heads, int n_seqs, int n_rows, int max_rows, int max_kv) {
+  Plan p{};
+  const int g = q_heads / heads;
+  p.T = 128 / g;
+  p.shared = max_rows > p.T;
+  const long long tt = p.shared ? 2 * p.T : p.T;
+  const long long by_rows = n_rows / tt + n_seqs, by_max = n_seqs * ((max_rows + tt - 1) / tt);
+  p.tiles = by_rows < by_max ? by_rows : by_max;
+  // about four CTAs per SM of 148 in turn, of at least 1024 keys each
+  const long long all = p.tiles * heads, keys = max_kv > 0 ? max_kv : 1;
+  long long n = all > 0 ? (4 * 148 + all - 1) / all : 1;
+  const long long most = (keys + 1023) / 1024;
+  n = n < 1 ? 1 : n > most ? most : n;
+  if (n > 256) n = 256;
+  long long len = (keys + n - 1) / n;
+  len = (len + 255) / 256 * 256;
+  p.stretch = static_cast<int>(len > 0x40000000ll ? 0x40000000ll : len);
+  p.n_stretch = static_cast<int>((keys + p.stretch - 1) / p.stretch);
+  if (p.n_stretch < 1) p.n_stretch = 1;
+  p.n_parts = p.n_stretch * (p.shared ? 1 : 2);
+  return p;
+}
+
+template <int D, int BITS, int G, bool SHARED>
+kvq_status run_tiles(const PagedArgs& a, long long grid, cudaStream_t st) {
+  constexpr uint32_t smem = Cfg<D, SHARED>::kSmem;
+  if (!set_smem_once(reinterpret_cast<const void*>(k_paged_tiles<D, BITS, G, SHARED>), smem)) return KVQ_ERR_CUDA;
+  k_paged_tiles<D, BITS, G, SHARED><<<static_cast<unsigned>(grid), kThreads, smem, st>>>(a);
+  return launch_status();
+}
+
+template <int D, int BITS, int G>
+kvq_status run(const PagedArgs& a, const Plan& p, cudaStream_t st) {
+  const long long grid = p.tiles * a.H * a.n_stretch;
+  if (grid >= (1ll << 31)) return KVQ_ERR_UNSUPPORTED;
+  const kvq_status s = p.shared ? run_tiles<D, BITS, G, true>(a, grid, st) : run_tiles<D, BITS, G, false>(a, grid, st);
+  if (s != KVQ_OK) return s;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>((static_cast<long long>(a.n_rows) * a.Hq + 7) / 8));
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, k_paged_merge<D, BITS>, a) != cudaSuccess) return KVQ_ERR_CUDA;
+  return launch_status();
+}
+
+size_t align256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 
 }  // namespace
 
-size_t attend_paged_workspace_bytes(const kvq_desc&, int, const kvq_paged&, int, int) { return 256; }
+size_t attend_paged_workspace_bytes(const kvq_desc& dk, int q_heads, const kvq_paged& pg, int max_rows, int max_kv) {
+  const Plan p = make_plan(q_heads, dk.heads, pg.n_seqs, pg.n_rows, max_rows, max_kv);
+  const size_t rows = static_cast<size_t>(pg.n_rows) * q_heads * p.n_parts;
+  return align256(rows * dk.head_dim * 4) + align256(rows * 8) + 256;
+}
 
 kvq_status launch_attend_paged(const kvq_desc& dk, const kvq_desc&, const void* q, int64_t q_stride, int q_heads,
                                const kvq_packed& kc, const kvq_tables& tk, const kvq_packed& vc, const kvq_tables& tv,
-                               const kvq_paged& pg, int max_rows, int, float scale, void* out, int64_t out_stride,
-                               void*, cudaStream_t st, const LaunchCtx&) {
+                               const kvq_paged& pg, int max_rows, int max_kv, float scale, void* out,
+                               int64_t out_stride, void* ws, cudaStream_t st, const LaunchCtx& ctx) {
+  const Plan p = make_plan(q_heads, dk.heads, pg.n_seqs, pg.n_rows, max_rows, max_kv);
   PagedArgs a{};
   a.S = pg.n_seqs;
   a.n_rows = pg.n_rows;
@@ -157,14 +694,17 @@ kvq_status launch_attend_paged(const kvq_desc& dk, const kvq_desc&, const void* 
   a.H = dk.heads;
   a.Hq = q_heads;
   a.g = q_heads / dk.heads;
-  a.ps = dk.t_cap;
+  a.T = p.T;
   a.n_pages = dk.batch;
   a.n_sink = dk.n_sink;
   a.rope = dk.rope;
   a.rope_rows = tk.rope_rows;
   a.rot = dk.rot == KVQ_ROT_FWHT_HEAD;
-  a.group = dk.group;
   a.max_rows = max_rows;
+  a.stretch = p.stretch;
+  a.n_stretch = p.n_stretch;
+  a.n_parts = p.n_parts;
+  a.div_ps = FastDiv(static_cast<uint32_t>(dk.t_cap));
   a.q_stride = q_stride;
   a.out_stride = out_stride;
   a.scale = scale;
@@ -184,10 +724,16 @@ kvq_status launch_attend_paged(const kvq_desc& dk, const kvq_desc&, const void* 
   a.vsz = static_cast<const __half2*>(vc.scale_zero);
   a.ksink = static_cast<const __half*>(kc.sink);
   a.vsink = static_cast<const __half*>(vc.sink);
-  const unsigned grid = static_cast<unsigned>((static_cast<long long>(pg.n_rows) * q_heads + 3) / 4);
-#define KVQ_CASE(D_, B_) \
-  if (dk.head_dim == D_ && dk.bits == B_) { k_paged_rows<D_, B_><<<grid, 128, 0, st>>>(a); return launch_status(); }
-  KVQ_CASE(128, 2) KVQ_CASE(128, 3) KVQ_CASE(128, 4) KVQ_CASE(64, 2) KVQ_CASE(64, 3) KVQ_CASE(64, 4)
+  const size_t rows = static_cast<size_t>(pg.n_rows) * q_heads * p.n_parts;
+  a.part_o = static_cast<float*>(ws);
+  a.part_s = reinterpret_cast<float2*>(static_cast<uint8_t*>(ws) + align256(rows * dk.head_dim * 4));
+  a.err = ctx.err;
+  a.wait_ns = ctx.wait_ns;
+#define KVQ_CASE(D_, B_, G_) \
+  if (dk.head_dim == D_ && dk.bits == B_ && dk.group == G_) return run<D_, B_, G_>(a, p, st);
+#define KVQ_BITS(D_, G_) KVQ_CASE(D_, 2, G_) KVQ_CASE(D_, 3, G_) KVQ_CASE(D_, 4, G_)
+  KVQ_BITS(128, 128) KVQ_BITS(128, 64) KVQ_BITS(128, 32) KVQ_BITS(64, 64) KVQ_BITS(64, 32)
+#undef KVQ_BITS
 #undef KVQ_CASE
   return KVQ_ERR_UNSUPPORTED;
 }

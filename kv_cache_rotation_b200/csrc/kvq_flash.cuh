@@ -155,31 +155,60 @@ struct RowStat {
   float m = -INFINITY, l = 0.0f;
 };
 
+// Columns [0, left) of a tile as bits.
+__device__ __forceinline__ uint32_t first_bits(int left, int at) {
+  return left >= at + 32 ? 0xffffffffu : left <= at ? 0u : (1u << (left - at)) - 1u;
+}
+
 // One score tile of a row (a thread's lane of tensor memory at `s_addr`, 128
-// fp32 columns), of which `seen(c)` allows column c when MASKED: the weights
+// fp32 columns), of which bit c of `seen` allows column c when MASKED: the weights
 // go back to the same columns, 16-bit, two to a column, and the sums at
 // `o_addr` (D fp32 columns, present when `have_o`) are rescaled if the
 // reference rises. Warp-uniform: every lane of the warp calls it. Each weight
 // is rounded once to T for the product (relative 2^-12 on average in fp16,
 // 2^-9 in bf16, where a sum over many keys averages it out); the row sum takes
-// the unrounded weights.
-template <typename T, int D, bool MASKED, typename Seen>
+// the unrounded weights. HOLD keeps the row's 128 scores in registers between
+// the maximum and the weights; without it they are read twice.
+template <typename T, int D, bool MASKED, bool HOLD>
 __device__ __forceinline__ void softmax_tile(uint32_t s_addr, uint32_t o_addr, bool have_o, float mul, RowStat& st,
-                                             Seen seen) {
-  uint32_t r[128];
+                                             const uint32_t (&seen)[4]) {
+  uint32_t r[HOLD ? 128 : 32];
+  auto load = [&](int c, uint32_t* x) {
+    tmem_ld32(s_addr + 32 * c, x);
+    tmem_wait_ld32(x);
+  };
+  auto mask = [&](int c, uint32_t* x) {
+    if constexpr (MASKED) {
+      uint32_t b = seen[c];
+      asm volatile("" : "+r"(b));  // the 128 tests are not kept from the first reading for the second
 #pragma unroll
-  for (int c = 0; c < 4; ++c) tmem_ld32(s_addr + 32 * c, r + 32 * c);
+      for (int i = 0; i < 32; ++i) x[i] = (b >> i) & 1u ? x[i] : 0xff800000u;
+    }
+  };
+  float mx = -INFINITY, mx2 = -INFINITY;
+  auto top = [&](const uint32_t* x) {
 #pragma unroll
-  for (int c = 0; c < 4; ++c) tmem_wait_ld32(r + 32 * c);
-  if constexpr (MASKED) {
+    for (int i = 0; i < 32; i += 4) {
+      mx = max3f(mx, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+      mx2 = max3f(mx2, __uint_as_float(x[i + 2]), __uint_as_float(x[i + 3]));
+    }
+  };
+  if constexpr (HOLD) {
 #pragma unroll
-    for (int c = 0; c < 128; ++c) r[c] = seen(c) ? r[c] : 0xff800000u;
-  }
-  float mx = fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1])), mx2 = fmaxf(__uint_as_float(r[2]), __uint_as_float(r[3]));
+    for (int c = 0; c < 4; ++c) tmem_ld32(s_addr + 32 * c, r + 32 * c);
 #pragma unroll
-  for (int c = 4; c < 128; c += 4) {
-    mx = max3f(mx, __uint_as_float(r[c]), __uint_as_float(r[c + 1]));
-    mx2 = max3f(mx2, __uint_as_float(r[c + 2]), __uint_as_float(r[c + 3]));
+    for (int c = 0; c < 4; ++c) {
+      tmem_wait_ld32(r + 32 * c);
+      mask(c, r + 32 * c);
+      top(r + 32 * c);
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      load(c, r);
+      mask(c, r);
+      top(r);
+    }
   }
   mx = fmaxf(mx, mx2) * mul;
   const bool raise = mx > st.m + kRaise;
@@ -205,9 +234,14 @@ __device__ __forceinline__ void softmax_tile(uint32_t s_addr, uint32_t o_addr, b
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
     uint32_t w[16];
+    uint32_t* x32 = r + (HOLD ? 32 * c : 0);
+    if constexpr (!HOLD) {
+      load(c, x32);
+      mask(c, x32);
+    }
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      const float2 x = fma2(f2(__uint_as_float(r[32 * c + 2 * i]), __uint_as_float(r[32 * c + 2 * i + 1])), mul2v, nm2);
+      const float2 x = fma2(f2(__uint_as_float(x32[2 * i]), __uint_as_float(x32[2 * i + 1])), mul2v, nm2);
       const float2 p = f2(exp2_fast(x.x), exp2_fast(x.y));
       if (i & 1) sum2 = add2(sum2, p); else sum = add2(sum, p);
       w[i] = Elem<T>::pack(p.x, p.y);
@@ -217,6 +251,48 @@ __device__ __forceinline__ void softmax_tile(uint32_t s_addr, uint32_t o_addr, b
   sum = add2(sum, sum2);
   st.l += sum.x + sum.y;
   tmem_wait_st();
+}
+
+// ---------------------------------------------------------------- packed rows
+// A tile of rows of one sequence.
+struct RowItem {
+  int seq, row0;  // its first packed row
+  int rows, len;  // its rows in all, and those that are computed (at most max_rows)
+  int q0;         // the tile's first row in the sequence
+};
+
+// Tile `idx` (of `tile` rows), counted from the last sequence's last tile backwards: under a causal
+// mask the long rows come first. One warp; item->len is 0 when there is no such tile. Offsets are cut
+// to [0, n_rows] and to ascending order.
+__device__ __forceinline__ void find_item(const int32_t* cu_rows, int n_seqs, int n_rows, int max_rows, int tile,
+                                          int idx, int lane, RowItem* item) {
+  if (lane == 0) item->len = 0;
+  __syncwarp();
+  for (int s0 = n_seqs - 1; s0 >= 0; s0 -= 32) {
+    const int s = s0 - lane;
+    int b = 0, rows = 0;
+    if (s >= 0) {
+      b = min(max(__ldg(cu_rows + s), 0), n_rows);
+      rows = min(max(__ldg(cu_rows + s + 1), b), n_rows) - b;
+    }
+    const int len = min(rows, max_rows), nt = (len + tile - 1) / tile;
+    int acc = nt;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, acc, o);
+      if (lane >= o) acc += y;
+    }
+    if (idx >= acc - nt && idx < acc) {
+      item->seq = s;
+      item->row0 = b;
+      item->rows = rows;
+      item->len = len;
+      item->q0 = (nt - 1 - (idx - (acc - nt))) * tile;
+    }
+    const int total = __shfl_sync(0xffffffffu, acc, 31);
+    if (idx < total) break;
+    idx -= total;
+  }
 }
 
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {

@@ -43,7 +43,8 @@ struct Cfg {
 struct Misc {
   uint64_t q_full, full[10], empty[10], s_full[2], p_full[2], o_full[2], loaded[kEdges], clean[kEdges];
   uint32_t tmem;
-  int row0, len, q0, dirty;
+  int dirty;
+  RowItem item;
   int first[3][128];  // first row with +inf, -inf, NaN in a channel of V, relative to the sequence
 };
 static_assert(sizeof(Misc) <= 2048, "fits behind the ring");
@@ -55,37 +56,6 @@ struct KernelArgs {
   uint64_t wait_ns;
   float mul;  // scale * log2(e)
 };
-
-// Item `idx` of KV-head-independent tiles, counted from the last sequence's last tile backwards: long
-// rows first. One warp; the result is in `m` (len 0: none).
-__device__ __forceinline__ void find_item(const PromptArgs& p, int TT, int idx, int lane, Misc* m) {
-  if (lane == 0) m->len = 0;
-  __syncwarp();
-  for (int s0 = p.n_seqs - 1; s0 >= 0; s0 -= 32) {
-    const int s = s0 - lane;
-    int b = 0, len = 0;
-    if (s >= 0) {
-      b = min(max(__ldg(p.cu_rows + s), 0), p.n_rows);
-      const int e = min(max(__ldg(p.cu_rows + s + 1), b), p.n_rows);
-      len = min(e - b, p.max_rows);
-    }
-    const int nt = (len + TT - 1) / TT;
-    int acc = nt;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, acc, o);
-      if (lane >= o) acc += y;
-    }
-    if (idx >= acc - nt && idx < acc) {
-      m->row0 = b;
-      m->len = len;
-      m->q0 = (nt - 1 - (idx - (acc - nt))) * TT;
-    }
-    const int total = __shfl_sync(0xffffffffu, acc, 31);
-    if (idx < total) break;
-    idx -= total;
-  }
-}
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -102,9 +72,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int h = static_cast<int>(blockIdx.x) - idx * a.p.heads;
   const int TT = 2 * a.T;
 
-  if (warp == 8) find_item(a.p, TT, idx, lane, m);
+  if (warp == 8) find_item(a.p.cu_rows, a.p.n_seqs, a.p.n_rows, a.p.max_rows, TT, idx, lane, &m->item);
   __syncthreads();
-  const int row0 = m->row0, len = m->len, q0 = m->q0;
+  const int row0 = m->item.row0, len = m->item.len, q0 = m->item.q0;
   if (len == 0) return;
   if (warp == 9) tmem_alloc(&m->tmem, 512);
   if (tid == 0) {
@@ -147,10 +117,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
       tc_fence_after();
       const int left = lim - 128 * i;  // columns seen
+      const uint32_t seen[4] = {first_bits(left, 0), first_bits(left, 32), first_bits(left, 64), first_bits(left, 96)};
       if (__any_sync(0xffffffffu, left < 128))
-        softmax_tile<T, D, true>(s_addr, o_addr, i > 0, a.mul, st, [&](int c) { return c < left; });
+        softmax_tile<T, D, true, true>(s_addr, o_addr, i > 0, a.mul, st, seen);
       else
-        softmax_tile<T, D, false>(s_addr, o_addr, i > 0, a.mul, st, [](int) { return true; });
+        softmax_tile<T, D, false, true>(s_addr, o_addr, i > 0, a.mul, st, seen);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&m->p_full[t]);
