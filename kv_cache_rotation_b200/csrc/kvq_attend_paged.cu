@@ -615,23 +615,495 @@ __global__ void __launch_bounds__(256) k_paged_merge(const PagedArgs a) {
                                                              (nat[warp][lane * C + c + 1] + own[c + 1]) * inv);
 }
 
+// ---------------------------------------------------------------- few rows
+// A decode step (max_rows * g <= 8 rows a KV head, head_dim 128, 2 or 4 bits)
+// is bound by instructions, not by the tensor cores, so it keeps the codes out
+// of shared-memory tiles: a warp takes blocks of 16 keys through its own ring of
+// cp.async stages, masks the codes in registers and multiplies them as they
+// are (mma.sync m16n8k16, fp16 in, fp32 out).
+//
+// A code field left at its bit of a 16-bit half is the fp16 subnormal c 2^p
+// 2^-24: one mask makes an operand register (two codes). 2^-p goes into the
+// query (scores) or is undone on the sums (values), both exactly; the other
+// operand is kept large (queries at 2^13, weights up to 2^15) so that its terms
+// stay normal. Every query value and every weight enters as two fp16 terms, hi
+// and lo, one column each (about 22 bits); fp32 statistics and sums.
+//
+//   scores: s = S_g sum_j q'_j c_j + Z_g sum_j q'_j per quantization group
+//           (A = 16 keys x 16 channels of codes, B = queries, N = 8: 4 rows x hi, lo)
+//   values: sum_n p_n y_n = sum_n (p_n S_n) c_n + sum_n p_n Z_n
+//           (A = 16 channels x 16 keys of codes, B = weights)
+// A weight p S is at most 2^15: the reference m follows s + log2 S (S >= 2^-30)
+// and is raised when that exceeds it by 2^8; p = 2^(s - m + 7).
+constexpr int kFewWarps = 8;
+constexpr int kFewThreads = 32 * kFewWarps;
+constexpr int kBlock = 16;
+constexpr float kFewUp = 7.0f;
+constexpr float kFewMinS = 9.3132257e-10f;  // 2^-30
+
+// Which codes a lane masks. Keys (scores): lane quarter tig holds kWords words of a
+// row, kPairs register pairs (code, code at +16 bits) each; pair p sits at bit
+// `bit` of the word, or of the word shifted right by `down`; its channels are ch
+// and ch + kFar. Values: lane group gr holds word(i) of two keys, merged to
+// registers of 16-bit halves; m-tile mt takes a code for row gr and one for row gr + 8.
+template <int BITS, int G>
+struct Map;
+template <int G>
+struct Map<2, G> {
+  static constexpr bool kFine = G == 32;  // two words a group
+  static constexpr int kWords = kFine ? 4 : 2, kPairs = kFine ? 4 : 8, kFar = 8;
+  static __device__ __forceinline__ int kword(int i, int tig) { return kFine ? 2 * i + (tig & 1) : tig + 4 * i; }
+  static __device__ __forceinline__ uint32_t kopen(uint32_t w, int tig) { return kFine ? w >> (8 * (tig >> 1)) : w; }
+  static __device__ __forceinline__ int kch(int i, int p, int tig) {
+    return 16 * kword(i, tig) + p + (kFine ? 4 * (tig >> 1) : 0);
+  }
+  static constexpr int kDown = 10;  // pairs 5 .. 7 are read after this shift
+  static __host__ __device__ constexpr bool shifted(int p) { return p >= 5; }
+  static __host__ __device__ constexpr int bit(int p) { return 2 * (p >= 5 ? p - 5 : p); }
+  static __host__ __device__ constexpr int group(int i) { return kFine ? i : i * 64 / G; }
+  // values
+  static constexpr int kVWords = G == 128 ? 1 : G == 64 ? 2 : 4;
+  static constexpr int kVRegs = G == 128 ? 2 : kVWords;
+  static __device__ __forceinline__ int vword(int i, int gr) {
+    return G == 128 ? gr : G == 64 ? 4 * i + (gr & 3) : 2 * i + (gr & 1);
+  }
+  // register r from the two keys' words
+  static __device__ __forceinline__ uint32_t vopen(int r, uint32_t a, uint32_t b, int gr) {
+    if (G == 128) return __byte_perm(a, b, r ? 0x7632 : 0x5410);
+    const bool hi = G == 64 ? gr >> 2 : (gr >> 1) & 1;
+    const uint32_t y = __byte_perm(a, b, hi ? 0x7632 : 0x5410);
+    return G == 64 ? y : y >> (8 * (gr >> 2));
+  }
+  static __host__ __device__ constexpr int vwordof(int r) { return G == 128 ? 0 : r; }
+  static __host__ __device__ constexpr int vreg(int mt, int row8) { return G == 128 ? row8 : G == 64 ? mt / 4 : mt / 2; }
+  static __host__ __device__ constexpr int vcode(int mt, int row8) {
+    return G == 128 ? mt : G == 64 ? mt % 4 + 4 * row8 : mt % 2 + 2 * row8;
+  }
+  static __device__ __forceinline__ int vch(int mt, int row8, int gr) {
+    if (G == 128) return 16 * gr + 8 * row8 + mt;
+    if (G == 64) return 16 * vword(mt / 4, gr) + 8 * (gr >> 2) + mt % 4 + 4 * row8;
+    return 16 * vword(mt / 2, gr) + 8 * ((gr >> 1) & 1) + 4 * (gr >> 2) + mt % 2 + 2 * row8;
+  }
+  static __host__ __device__ constexpr int vgroup(int mt) { return G == 128 ? 0 : G == 64 ? mt / 4 : mt / 2; }
+};
+template <int G>
+struct Map<4, G> {
+  static constexpr bool kFine = G == 32;
+  static constexpr int kWords = 4, kPairs = 4, kFar = 4, kDown = 8;
+  static __device__ __forceinline__ int kword(int i, int tig) { return tig + 4 * i; }
+  static __device__ __forceinline__ uint32_t kopen(uint32_t w, int) { return w; }
+  static __device__ __forceinline__ int kch(int i, int p, int tig) { return 8 * kword(i, tig) + p; }
+  static __host__ __device__ constexpr bool shifted(int p) { return p >= 2; }
+  static __host__ __device__ constexpr int bit(int p) { return 4 * (p & 1); }
+  static __host__ __device__ constexpr int group(int i) { return 32 * i / G; }
+  static constexpr int kVWords = kFine ? 4 : 2, kVRegs = 4;
+  static __device__ __forceinline__ int vword(int i, int gr) { return kFine ? 4 * i + (gr & 3) : gr + 8 * i; }
+  static __device__ __forceinline__ uint32_t vopen(int r, uint32_t a, uint32_t b, int gr) {
+    const bool hi = kFine ? gr >> 2 : r & 1;
+    return __byte_perm(a, b, hi ? 0x7632 : 0x5410);
+  }
+  static __host__ __device__ constexpr int vwordof(int r) { return kFine ? r : r / 2; }
+  static __host__ __device__ constexpr int vreg(int mt, int row8) { return kFine ? mt / 2 : 2 * (mt / 4) + row8; }
+  static __host__ __device__ constexpr int vcode(int mt, int row8) { return kFine ? mt % 2 + 2 * row8 : mt % 4; }
+  static __device__ __forceinline__ int vch(int mt, int row8, int gr) {
+    return kFine ? 8 * vword(mt / 2, gr) + 4 * (gr >> 2) + mt % 2 + 2 * row8 : 8 * vword(mt / 4, gr) + 4 * row8 + mt % 4;
+  }
+  static __host__ __device__ constexpr int vgroup(int mt) { return kFine ? mt / 2 : G == 64 ? mt / 4 : 0; }
+};
+
+template <int BITS, int G>
+struct FewCfg {
+  static constexpr int kRec = 128 * BITS / 8, kNG = 128 / G;
+  static constexpr int kStage = 2 * kBlock * (kRec + 4 * kNG) + 16;  // key codes, value codes, their (S, Z), key mask
+  static constexpr int kStages = BITS == 2 ? 6 : 4;
+  static constexpr int kSmem = kFewWarps * kStages * kStage;
+};
+
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, uint32_t n) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void mma_h(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                      uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// x as fp16 hi + lo (hi in the low half).
+__device__ __forceinline__ uint32_t hi_lo(float x) {
+  const __half hi = __float2half_rn(x);
+  const __half lo = __float2half_rn(x - __half2float(hi));
+  return static_cast<uint32_t>(__half_as_ushort(hi)) | (static_cast<uint32_t>(__half_as_ushort(lo)) << 16);
+}
+__device__ __forceinline__ float2 h2f2(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
+
+// NT: column tiles, 4 rows each. One CTA per (stretch of keys, KV head, sequence).
+template <int BITS, int G, int NT>
+__global__ void __launch_bounds__(kFewThreads, NT == 1 ? 2 : 1) k_paged_few(const PagedArgs a) {
+  using C = FewCfg<BITS, G>;
+  using M = Map<BITS, G>;
+  constexpr int D = 128, NG = C::kNG, RB = C::kRec, ST = C::kStages, R = 4 * NT;
+  extern __shared__ __align__(128) uint8_t few_smem[];
+  __shared__ float qrow[R][D];
+  __shared__ float qmul[R], qsum[R][NG];
+  __shared__ float wm[kFewWarps][R], wl[kFewWarps][R], wz[kFewWarps][R][NG];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int gr = lane >> 2, tig = lane & 3;
+  unsigned rest = blockIdx.x;
+  const int z = static_cast<int>(rest % static_cast<unsigned>(a.n_stretch));
+  rest /= static_cast<unsigned>(a.n_stretch);
+  const int h = static_cast<int>(rest % static_cast<unsigned>(a.H));
+  const int s = static_cast<int>(rest / static_cast<unsigned>(a.H));
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int row0 = min(max(__ldg(a.cu_rows + s), 0), a.n_rows);
+  const int m_rows = min(max(__ldg(a.cu_rows + s + 1), row0), a.n_rows) - row0;
+  const int tokens = min(m_rows, a.max_rows);
+  const int cached = max(__ldg(a.kv_len + s), 0);
+  const int kv = min(cached, sat_pages(a.max_pages, static_cast<int>(a.div_ps.d)));
+  const int pos0 = cached - m_rows;
+  const long long kb = static_cast<long long>(z) * a.stretch;
+  const long long ke = z + 1 == a.n_stretch ? 0x7fffffffll : kb + a.stretch;
+  const int k0 = static_cast<int>(min(kb, 0x7fffffffll));
+  const int k1 = static_cast<int>(min(ke, static_cast<long long>(min(kv, pos0 + tokens))));
+  if (tokens == 0 || k1 <= k0) return;  // no row sees a key here: the merge does not look
+  const int n_rows = tokens * a.g;      // at most R
+  const int blocks = (k1 - k0 + kBlock - 1) / kBlock;
+  const int mine = blocks > warp ? (blocks - warp + kFewWarps - 1) / kFewWarps : 0;  // blocks warp + 8 i
+
+  // ---- the ring: lane copies half a record of key lane / 2, and its (S, Z) (even lanes keys, odd lanes values)
+  const uint32_t wbase = smem_u32(few_smem) + warp * (ST * C::kStage);
+  const uint8_t* const wgen = few_smem + warp * (ST * C::kStage);
+  const int32_t* table = a.block_table + static_cast<size_t>(s) * a.max_pages;
+  const int kt = lane >> 1, kh = lane & 1;
+  auto page_of = [&](int i) {
+    if (i >= mine) return -1;
+    const int pos = k0 + (warp + kFewWarps * i) * kBlock + kt;
+    if (pos >= k1 || pos < a.n_sink) return -1;
+    const int pg = __ldg(table + a.div_ps.div(static_cast<uint32_t>(pos)));
+    return pg < a.n_pages ? pg : -1;
+  };
+  auto issue = [&](int i, int pg) {  // block i of this warp, the page of this lane's key
+    if (i < mine) {
+      const uint32_t sb = wbase + (i % ST) * C::kStage;
+      const uint32_t pos = static_cast<uint32_t>(k0 + (warp + kFewWarps * i) * kBlock + kt);
+      const size_t rec = pg < 0 ? 0 : (static_cast<size_t>(pg) * a.H + h) * a.div_ps.d + a.div_ps.mod(pos, a.div_ps.div(pos));
+      const uint32_t n = pg < 0 ? 0u : 16u;
+      const uint8_t* kc = a.kcodes + rec * RB + kh * (RB / 2);
+      const uint8_t* vc = a.vcodes + rec * RB + kh * (RB / 2);
+      const uint32_t at = sb + kt * RB + kh * (RB / 2);
+#pragma unroll
+      for (int c = 0; c < RB / 32; ++c) {
+        cp_async16(at + 16 * c, kc + 16 * c, n);
+        cp_async16(at + kBlock * RB + 16 * c, vc + 16 * c, n);
+      }
+      const __half2* sz = (kh ? a.vsz : a.ksz) + rec * NG;
+      const uint32_t zt = sb + 2 * kBlock * RB + (kh * kBlock + kt) * 4 * NG;
+      if constexpr (NG == 1) cp_async4(zt, sz, pg < 0 ? 0u : 4u);
+      else if constexpr (NG == 2) cp_async8(zt, sz, pg < 0 ? 0u : 8u);
+      else cp_async16(zt, sz, n);
+      const uint32_t seen = __ballot_sync(0xffffffffu, pg >= 0);  // two bits a key
+      if (lane == 0) asm volatile("st.shared.u32 [%0], %1;" ::"r"(sb + 2 * kBlock * (RB + 4 * NG)), "r"(seen) : "memory");
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < ST; ++i) issue(i, page_of(i));
+  int pn = page_of(ST);
+
+  // ---- query rows: rotated, scaled by a power of two to [2^13, 2^14)
+  for (int r = warp; r < R; r += kFewWarps) {
+    float x[4], top = 0.0f;
+    const int tok = r / a.g, j = r - tok * a.g;
+    const __half* qp = a.q + (static_cast<int64_t>(row0) + tok) * a.q_stride + (h * a.g + j) * D;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const int ch = 4 * lane + c;
+      x[c] = r < n_rows ? __half2float(qp[a.kperm ? a.kperm[h * D + ch] & (D - 1) : ch]) : 0.0f;
+    }
+    if (a.rot) {
+      warp_fwht<4>(x, lane);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) x[c] *= a.rscale;
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c) top = fmaxf(top, fabsf(x[c]));
+    top = all_max(top);
+    const int e = top > 0.0f && top < INFINITY ? static_cast<int>(__float_as_uint(top) >> 23) - 127 : 0;
+    const float up = __uint_as_float(static_cast<uint32_t>(127 + 13 - e) << 23);
+    float sum = 0.0f;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      qrow[r][4 * lane + c] = x[c] * up;
+      sum += x[c];
+    }
+    // lanes of a group: G / 4
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1)
+      if (4 * o < G) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const float unit = a.scale * 1.4426950408889634f;
+    if (lane % (G / 4) == 0) qsum[r][lane / (G / 4)] = sum * unit;
+    if (lane == 0) qmul[r] = unit * __uint_as_float(static_cast<uint32_t>(127 - 13 + e) << 23) * 16777216.0f;
+  }
+  __syncthreads();
+  // B fragments of the scores: column gr of tile t is row 4 t + gr / 2, term gr & 1
+  uint32_t bq[8][NT][2];
+  float mul[NT], qz[NT][NG];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const float* q = qrow[4 * t + (gr >> 1)];
+#pragma unroll
+    for (int ks = 0; ks < 8; ++ks)
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        constexpr int PK = M::kPairs / 2;  // k-steps of a word
+        const int i = ks / PK, p = 2 * (ks % PK) + b, ch = M::kch(i, p, tig);
+        const float down = 1.0f / static_cast<float>(1 << M::bit(p));
+        const uint32_t x = hi_lo(q[ch] * down), y = hi_lo(q[ch + M::kFar] * down);
+        bq[ks][t][b] = __byte_perm(x, y, (gr & 1) ? 0x7632 : 0x5410);
+      }
+    mul[t] = qmul[4 * t + tig];
+#pragma unroll
+    for (int k = 0; k < NG; ++k) qz[t][k] = qsum[4 * t + tig][k];
+  }
+  int lim[NT];  // keys [0, lim) are seen by this lane's row of each tile
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int r = 4 * t + tig;
+    lim[t] = r < n_rows ? pos0 + r / a.g + 1 : 0x7fffffff;
+  }
+
+  float acc[8][NT][4], mr[NT], lr[NT], zr[NT][NG];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    mr[t] = -INFINITY;
+    lr[t] = 0.0f;
+#pragma unroll
+    for (int k = 0; k < NG; ++k) zr[t][k] = 0.0f;
+#pragma unroll
+    for (int mt = 0; mt < 8; ++mt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[mt][t][e] = 0.0f;
+  }
+  const int srcA = 8 * tig + (gr >> 1), srcB = srcA + 4;
+  const uint32_t sel = (gr & 1) ? 0x7632u : 0x5410u;
+
+  for (int i = 0; i < mine; ++i) {
+    cp_async_wait_group<ST - 1>();
+    __syncwarp();
+    const uint8_t* st = wgen + (i % ST) * C::kStage;
+    const uint8_t* kz = st + 2 * kBlock * RB;
+    const uint8_t* vz = kz + kBlock * 4 * NG;
+    const int n0 = k0 + (warp + kFewWarps * i) * kBlock;
+    const uint32_t seen = *reinterpret_cast<const uint32_t*>(st + 2 * kBlock * (RB + 4 * NG));
+    // ---- scores of keys gr and gr + 8
+    float sc[NG][NT][4];
+#pragma unroll
+    for (int k = 0; k < NG; ++k)
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sc[k][t][e] = 0.0f;
+#pragma unroll
+    for (int w = 0; w < M::kWords; ++w) {
+      const uint32_t wa = M::kopen(*reinterpret_cast<const uint32_t*>(st + gr * RB + 4 * M::kword(w, tig)), tig);
+      const uint32_t wb = M::kopen(*reinterpret_cast<const uint32_t*>(st + (gr + 8) * RB + 4 * M::kword(w, tig)), tig);
+      const uint32_t da = wa >> M::kDown, db = wb >> M::kDown;
+#pragma unroll
+      for (int p = 0; p < M::kPairs; p += 2) {
+        constexpr uint32_t F = (1u << BITS) - 1u;
+        const uint32_t m0 = (F | F << 16) << M::bit(p), m1 = (F | F << 16) << M::bit(p + 1);
+        const uint32_t a0 = (M::shifted(p) ? da : wa) & m0, a1 = (M::shifted(p) ? db : wb) & m0;
+        const uint32_t a2 = (M::shifted(p + 1) ? da : wa) & m1, a3 = (M::shifted(p + 1) ? db : wb) & m1;
+        const int ks = w * (M::kPairs / 2) + p / 2;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) mma_h(sc[M::group(w)][t], a0, a1, a2, a3, bq[ks][t][0], bq[ks][t][1]);
+      }
+    }
+    uint32_t ka[NG], kb2[NG], va[NG], vb[NG];
+#pragma unroll
+    for (int k = 0; k < NG; ++k) {
+      ka[k] = *reinterpret_cast<const uint32_t*>(kz + (gr * NG + k) * 4);
+      kb2[k] = *reinterpret_cast<const uint32_t*>(kz + ((gr + 8) * NG + k) * 4);
+      va[k] = *reinterpret_cast<const uint32_t*>(vz + (gr * NG + k) * 4);
+      vb[k] = *reinterpret_cast<const uint32_t*>(vz + ((gr + 8) * NG + k) * 4);
+    }
+    // log2 of the largest value scale of each key, for the range of its weights
+    float ta = kFewMinS, tb = kFewMinS;
+    float2 va2[NG], vb2[NG];
+#pragma unroll
+    for (int k = 0; k < NG; ++k) {
+      va2[k] = h2f2(va[k]);
+      vb2[k] = h2f2(vb[k]);
+      ta = fmaxf(ta, va2[k].x);
+      tb = fmaxf(tb, vb2[k].x);
+    }
+    float lga, lgb;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(lga) : "f"(ta));
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(lgb) : "f"(tb));
+    uint32_t wa2[NT][NG], wb2[NT][NG];
+    float sa[NT], sb[NT];
+    bool raise = false;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      sa[t] = sb[t] = 0.0f;
+#pragma unroll
+      for (int k = 0; k < NG; ++k) {
+        const float2 za = h2f2(ka[k]), zb = h2f2(kb2[k]);
+        sa[t] = fmaf(za.x * mul[t], sc[k][t][0] + sc[k][t][1], fmaf(za.y, qz[t][k], sa[t]));
+        sb[t] = fmaf(zb.x * mul[t], sc[k][t][2] + sc[k][t][3], fmaf(zb.y, qz[t][k], sb[t]));
+      }
+      if (seen != 0xffffffffu || n0 + kBlock > lim[t]) {
+        if (!((seen >> (2 * gr)) & 1u) || n0 + gr >= lim[t]) sa[t] = -INFINITY;
+        if (!((seen >> (2 * gr + 16)) & 1u) || n0 + gr + 8 >= lim[t]) sb[t] = -INFINITY;
+      }
+      raise |= fmaxf(sa[t] + lga, sb[t] + lgb) > mr[t] + kRaise;
+    }
+    if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        float top = fmaxf(sa[t] + lga, sb[t] + lgb);
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+        if (top > mr[t] + kRaise) {  // the same for the eight lanes of a row
+          const float f = exp2_fast(mr[t] - top);
+          mr[t] = top;
+          lr[t] *= f;
+#pragma unroll
+          for (int k = 0; k < NG; ++k) zr[t][k] *= f;
+#pragma unroll
+          for (int mt = 0; mt < 8; ++mt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[mt][t][e] *= f;
+        }
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const float ref = mr[t] == -INFINITY ? 0.0f : kFewUp - mr[t];
+      const float pa = exp2_fast(sa[t] + ref), pb = exp2_fast(sb[t] + ref);
+      lr[t] += pa + pb;
+#pragma unroll
+      for (int k = 0; k < NG; ++k) {
+        zr[t][k] = fmaf(pa, va2[k].y, fmaf(pb, vb2[k].y, zr[t][k]));
+        const uint32_t xa = hi_lo(pa * va2[k].x), xb = hi_lo(pb * vb2[k].x);
+        // keys 2 tig, 2 tig + 1 (and + 8) of column gr
+        wa2[t][k] = __byte_perm(__shfl_sync(0xffffffffu, xa, srcA), __shfl_sync(0xffffffffu, xa, srcB), sel);
+        wb2[t][k] = __byte_perm(__shfl_sync(0xffffffffu, xb, srcA), __shfl_sync(0xffffffffu, xb, srcB), sel);
+      }
+    }
+    // ---- values
+    {
+      const uint8_t* v0 = st + kBlock * RB + 2 * tig * RB;
+      uint32_t y[2][M::kVRegs], yd[2][M::kVRegs];
+#pragma unroll
+      for (int w = 0; w < M::kVWords; ++w) {
+        const int at = 4 * M::vword(w, gr);
+        const uint32_t u0 = *reinterpret_cast<const uint32_t*>(v0 + at), u1 = *reinterpret_cast<const uint32_t*>(v0 + RB + at);
+        const uint32_t u8 = *reinterpret_cast<const uint32_t*>(v0 + 8 * RB + at), u9 = *reinterpret_cast<const uint32_t*>(v0 + 9 * RB + at);
+#pragma unroll
+        for (int r = 0; r < M::kVRegs; ++r)
+          if (M::vwordof(r) == w) {
+            y[0][r] = M::vopen(r, u0, u1, gr);
+            y[1][r] = M::vopen(r, u8, u9, gr);
+            yd[0][r] = y[0][r] >> M::kDown;
+            yd[1][r] = y[1][r] >> M::kDown;
+          }
+      }
+#pragma unroll
+      for (int mt = 0; mt < 8; ++mt) {
+        constexpr uint32_t F = (1u << BITS) - 1u;
+        uint32_t x[2][2];  // [row gr / gr + 8][keys 2 tig / + 8]
+#pragma unroll
+        for (int r8 = 0; r8 < 2; ++r8)
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            const int c = M::vcode(mt, r8), r = M::vreg(mt, r8);
+            x[r8][b] = (M::shifted(c) ? yd[b][r] : y[b][r]) & ((F | F << 16) << M::bit(c));
+          }
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+          mma_h(acc[mt][t], x[0][0], x[1][0], x[0][1], x[1][1], wa2[t][M::vgroup(mt)], wb2[t][M::vgroup(mt)]);
+      }
+    }
+    __syncwarp();
+    issue(i + ST, pn);
+    pn = page_of(i + ST + 1);
+  }
+  cp_async_wait_all();
+
+  // ---- the warps' sums, joined in a fixed order
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) {
+      lr[t] += __shfl_xor_sync(0xffffffffu, lr[t], o);
+#pragma unroll
+      for (int k = 0; k < NG; ++k) zr[t][k] += __shfl_xor_sync(0xffffffffu, zr[t][k], o);
+    }
+    if (gr == 0) {
+      wm[warp][4 * t + tig] = mr[t];
+      wl[warp][4 * t + tig] = lr[t];
+#pragma unroll
+      for (int k = 0; k < NG; ++k) wz[warp][4 * t + tig][k] = zr[t][k];
+    }
+  }
+  __syncthreads();  // every warp has left its ring: it holds the sums now
+  float* sums = reinterpret_cast<float*>(few_smem);  // [warp][row][channel]
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int r = 4 * t + tig;
+    float top = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kFewWarps; ++w) top = fmaxf(top, wm[w][r]);
+    const float f = mr[t] == -INFINITY ? 0.0f : exp2_fast(mr[t] - top);
+#pragma unroll
+    for (int mt = 0; mt < 8; ++mt)
+#pragma unroll
+      for (int r8 = 0; r8 < 2; ++r8) {
+        const float up = 16777216.0f / static_cast<float>(1 << M::bit(M::vcode(mt, r8)));
+        sums[(warp * R + r) * D + M::vch(mt, r8, gr)] = (acc[mt][t][2 * r8] + acc[mt][t][2 * r8 + 1]) * up * f;
+      }
+  }
+  __syncthreads();
+  for (int e = tid; e < n_rows * D; e += kFewThreads) {
+    const int r = e / D, ch = e % D;
+    float top = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kFewWarps; ++w) top = fmaxf(top, wm[w][r]);
+    float o = 0.0f, l = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kFewWarps; ++w) {
+      if (wm[w][r] == -INFINITY && wl[w][r] == 0.0f) continue;
+      const float f = exp2_fast(wm[w][r] - top);
+      o += sums[(w * R + r) * D + ch] + wz[w][r][ch / G] * f;
+      l = fmaf(wl[w][r], f, l);
+    }
+    const size_t at = static_cast<size_t>(z) * (static_cast<size_t>(a.n_rows) * a.Hq) +
+                      (static_cast<size_t>(row0) + r / a.g) * a.Hq + h * a.g + r % a.g;
+    a.part_o[at * D + tile_pos<BITS>(ch)] = o;
+    if (ch == 0) a.part_s[at] = make_float2(top - kFewUp, l);
+  }
+}
+
 // How a call's work is cut: row tiles, and stretches of keys per tile.
 struct Plan {
-  bool shared;
+  bool shared, few;
   int T, stretch, n_stretch, n_parts;
   long long tiles;
 };
-Plan make_plan(int q_heads, int heads, int n_seqs, int n_rows, int max_rows, int max_kv) {
+Plan make_plan(const kvq_desc& d, int q_heads, int n_seqs, int n_rows, int max_rows, int max_kv) {
+  const int heads = d.heads;
   Plan p{};
   const int g = q_heads / heads;
   p.T = 128 / g;
+  p.few = d.head_dim == 128 && d.bits != 3 && static_cast<long long>(max_rows) * g <= 8;
   p.shared = max_rows > p.T;
   const long long tt = p.shared ? 2 * p.T : p.T;
   const long long by_rows = n_rows / tt + n_seqs, by_max = n_seqs * ((max_rows + tt - 1) / tt);
-  p.tiles = by_rows < by_max ? by_rows : by_max;
+  p.tiles = p.few ? n_seqs : by_rows < by_max ? by_rows : by_max;
   // about four CTAs per SM of 148 in turn, of at least 1024 keys each
   const long long all = p.tiles * heads, keys = max_kv > 0 ? max_kv : 1;
-  long long n = all > 0 ? (4 * 148 + all - 1) / all : 1;
+  long long n = all > 0 ? 4 * 148 / all : 1;
   const long long most = (keys + 1023) / 1024;
   n = n < 1 ? 1 : n > most ? most : n;
   if (n > 256) n = 256;
@@ -640,7 +1112,7 @@ Plan make_plan(int q_heads, int heads, int n_seqs, int n_rows, int max_rows, int
   p.stretch = static_cast<int>(len > 0x40000000ll ? 0x40000000ll : len);
   p.n_stretch = static_cast<int>((keys + p.stretch - 1) / p.stretch);
   if (p.n_stretch < 1) p.n_stretch = 1;
-  p.n_parts = p.n_stretch * (p.shared ? 1 : 2);
+  p.n_parts = p.n_stretch * (p.shared || p.few ? 1 : 2);
   return p;
 }
 
@@ -652,11 +1124,26 @@ kvq_status run_tiles(const PagedArgs& a, long long grid, cudaStream_t st) {
   return launch_status();
 }
 
+template <int BITS, int G, int NT>
+kvq_status run_few(const PagedArgs& a, long long grid, cudaStream_t st) {
+  constexpr int smem = FewCfg<BITS, G>::kSmem;
+  static_assert(smem >= kFewWarps * 4 * NT * 128 * 4, "the ring holds the warps' sums at the end");
+  if (!set_smem_once(reinterpret_cast<const void*>(k_paged_few<BITS, G, NT>), smem)) return KVQ_ERR_CUDA;
+  k_paged_few<BITS, G, NT><<<static_cast<unsigned>(grid), kFewThreads, smem, st>>>(a);
+  return launch_status();
+}
+
 template <int D, int BITS, int G>
 kvq_status run(const PagedArgs& a, const Plan& p, cudaStream_t st) {
   const long long grid = p.tiles * a.H * a.n_stretch;
   if (grid >= (1ll << 31)) return KVQ_ERR_UNSUPPORTED;
-  const kvq_status s = p.shared ? run_tiles<D, BITS, G, true>(a, grid, st) : run_tiles<D, BITS, G, false>(a, grid, st);
+  kvq_status s;
+  if constexpr (D == 128 && BITS != 3) {
+    s = p.few ? (a.max_rows * a.g <= 4 ? run_few<BITS, G, 1>(a, grid, st) : run_few<BITS, G, 2>(a, grid, st))
+              : p.shared ? run_tiles<D, BITS, G, true>(a, grid, st) : run_tiles<D, BITS, G, false>(a, grid, st);
+  } else {
+    s = p.shared ? run_tiles<D, BITS, G, true>(a, grid, st) : run_tiles<D, BITS, G, false>(a, grid, st);
+  }
   if (s != KVQ_OK) return s;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>((static_cast<long long>(a.n_rows) * a.Hq + 7) / 8));
@@ -676,7 +1163,7 @@ size_t align256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 }  // namespace
 
 size_t attend_paged_workspace_bytes(const kvq_desc& dk, int q_heads, const kvq_paged& pg, int max_rows, int max_kv) {
-  const Plan p = make_plan(q_heads, dk.heads, pg.n_seqs, pg.n_rows, max_rows, max_kv);
+  const Plan p = make_plan(dk, q_heads, pg.n_seqs, pg.n_rows, max_rows, max_kv);
   const size_t rows = static_cast<size_t>(pg.n_rows) * q_heads * p.n_parts;
   return align256(rows * dk.head_dim * 4) + align256(rows * 8) + 256;
 }
@@ -685,7 +1172,7 @@ kvq_status launch_attend_paged(const kvq_desc& dk, const kvq_desc&, const void* 
                                const kvq_packed& kc, const kvq_tables& tk, const kvq_packed& vc, const kvq_tables& tv,
                                const kvq_paged& pg, int max_rows, int max_kv, float scale, void* out,
                                int64_t out_stride, void* ws, cudaStream_t st, const LaunchCtx& ctx) {
-  const Plan p = make_plan(q_heads, dk.heads, pg.n_seqs, pg.n_rows, max_rows, max_kv);
+  const Plan p = make_plan(dk, q_heads, pg.n_seqs, pg.n_rows, max_rows, max_kv);
   PagedArgs a{};
   a.S = pg.n_seqs;
   a.n_rows = pg.n_rows;
