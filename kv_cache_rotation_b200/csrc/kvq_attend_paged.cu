@@ -17,6 +17,7 @@
 // k_paged_merge: one warp per row and query head joins them with the sinks and
 // turns the result back.
 #include <math.h>
+#include <stdlib.h>
 
 #include "kvq_flash.cuh"
 #include "kvq_internal.h"
@@ -31,6 +32,7 @@ constexpr int kMasks = 8;  // key masks kept: more tiles than are in flight
 struct PagedArgs {
   int S, n_rows, max_pages, sink_rows, H, Hq, g, T, n_pages, n_sink, rope, rope_rows, rot, max_rows;
   int stretch, n_stretch, n_parts;  // keys of a CTA, CTAs along the keys, partial results per row
+  int step_page, step_off;          // 128 keys in pages and a rest
   FastDiv div_ps;
   int64_t q_stride, out_stride;
   float scale, rscale;
@@ -233,10 +235,10 @@ __device__ __forceinline__ float all_max(float v) {
   return v;
 }
 
-// Positions that a block_table row covers.
+// Positions that a block_table row covers, a few blocks below 2^31 so that steps past the end fit.
 __device__ __forceinline__ int sat_pages(int pages, int ps) {
   const long long v = static_cast<long long>(pages) * ps;
-  return v > 0x7fffffffll ? 0x7fffffff : static_cast<int>(v);
+  return v > 0x7ffffe00ll ? 0x7ffffe00 : static_cast<int>(v);
 }
 
 template <int D, int BITS, int G, bool SHARED>
@@ -638,6 +640,7 @@ __global__ void __launch_bounds__(256) k_paged_merge(const PagedArgs a) {
 constexpr int kFewWarps = 8;
 constexpr int kFewThreads = 32 * kFewWarps;
 constexpr int kBlock = 16;
+static_assert(kFewWarps * kBlock == 128, "a warp's next block is 128 keys on");
 constexpr float kFewUp = 7.0f;
 constexpr float kFewMinS = 9.3132257e-10f;  // 2^-30
 
@@ -652,7 +655,9 @@ template <int G>
 struct Map<2, G> {
   static constexpr bool kFine = G == 32;  // two words a group
   static constexpr int kWords = kFine ? 4 : 2, kPairs = kFine ? 4 : 8, kFar = 8;
-  static __device__ __forceinline__ int kword(int i, int tig) { return kFine ? 2 * i + (tig & 1) : tig + 4 * i; }
+  static __device__ __forceinline__ int kword(int i, int tig) {
+    return kFine ? 2 * i + (tig & 1) : G == 128 ? 2 * tig + i : tig + 4 * i;  // one group: adjacent words, one load
+  }
   static __device__ __forceinline__ uint32_t kopen(uint32_t w, int tig) { return kFine ? w >> (8 * (tig >> 1)) : w; }
   static __device__ __forceinline__ int kch(int i, int p, int tig) {
     return 16 * kword(i, tig) + p + (kFine ? 4 * (tig >> 1) : 0);
@@ -690,7 +695,7 @@ template <int G>
 struct Map<4, G> {
   static constexpr bool kFine = G == 32;
   static constexpr int kWords = 4, kPairs = 4, kFar = 4, kDown = 8;
-  static __device__ __forceinline__ int kword(int i, int tig) { return tig + 4 * i; }
+  static __device__ __forceinline__ int kword(int i, int tig) { return G == 128 ? 4 * tig + i : tig + 4 * i; }
   static __device__ __forceinline__ uint32_t kopen(uint32_t w, int) { return w; }
   static __device__ __forceinline__ int kch(int i, int p, int tig) { return 8 * kword(i, tig) + p; }
   static __host__ __device__ constexpr bool shifted(int p) { return p >= 2; }
@@ -745,7 +750,7 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 2 : 1) k_paged_few(cons
   extern __shared__ __align__(128) uint8_t few_smem[];
   __shared__ float qrow[R][D];
   __shared__ float qmul[R], qsum[R][NG];
-  __shared__ float wm[kFewWarps][R], wl[kFewWarps][R], wz[kFewWarps][R][NG];
+  __shared__ float wm[kFewWarps][R], wl[kFewWarps][R];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int gr = lane >> 2, tig = lane & 3;
   unsigned rest = blockIdx.x;
@@ -774,40 +779,56 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 2 : 1) k_paged_few(cons
   const uint8_t* const wgen = few_smem + warp * (ST * C::kStage);
   const int32_t* table = a.block_table + static_cast<size_t>(s) * a.max_pages;
   const int kt = lane >> 1, kh = lane & 1;
-  auto page_of = [&](int i) {
-    if (i >= mine) return -1;
-    const int pos = k0 + (warp + kFewWarps * i) * kBlock + kt;
-    if (pos >= k1 || pos < a.n_sink) return -1;
-    const int pg = __ldg(table + a.div_ps.div(static_cast<uint32_t>(pos)));
-    return pg < a.n_pages ? pg : -1;
+  // this lane's key of the next block to look up: position, entry of the table, offset in the page
+  int pos = k0 + warp * kBlock + kt, entry = static_cast<int>(a.div_ps.div(static_cast<uint32_t>(pos)));
+  int off = static_cast<int>(a.div_ps.mod(static_cast<uint32_t>(pos), entry));
+  const int ps = static_cast<int>(a.div_ps.d);
+  struct Key {
+    int page, off;
   };
-  auto issue = [&](int i, int pg) {  // block i of this warp, the page of this lane's key
-    if (i < mine) {
-      const uint32_t sb = wbase + (i % ST) * C::kStage;
-      const uint32_t pos = static_cast<uint32_t>(k0 + (warp + kFewWarps * i) * kBlock + kt);
-      const size_t rec = pg < 0 ? 0 : (static_cast<size_t>(pg) * a.H + h) * a.div_ps.d + a.div_ps.mod(pos, a.div_ps.div(pos));
-      const uint32_t n = pg < 0 ? 0u : 16u;
-      const uint8_t* kc = a.kcodes + rec * RB + kh * (RB / 2);
-      const uint8_t* vc = a.vcodes + rec * RB + kh * (RB / 2);
-      const uint32_t at = sb + kt * RB + kh * (RB / 2);
-#pragma unroll
-      for (int c = 0; c < RB / 32; ++c) {
-        cp_async16(at + 16 * c, kc + 16 * c, n);
-        cp_async16(at + kBlock * RB + 16 * c, vc + 16 * c, n);
-      }
-      const __half2* sz = (kh ? a.vsz : a.ksz) + rec * NG;
-      const uint32_t zt = sb + 2 * kBlock * RB + (kh * kBlock + kt) * 4 * NG;
-      if constexpr (NG == 1) cp_async4(zt, sz, pg < 0 ? 0u : 4u);
-      else if constexpr (NG == 2) cp_async8(zt, sz, pg < 0 ? 0u : 8u);
-      else cp_async16(zt, sz, n);
-      const uint32_t seen = __ballot_sync(0xffffffffu, pg >= 0);  // two bits a key
-      if (lane == 0) asm volatile("st.shared.u32 [%0], %1;" ::"r"(sb + 2 * kBlock * (RB + 4 * NG)), "r"(seen) : "memory");
+  auto look_up = [&](Key& k) {  // the page of a key that is not to be read is -1
+    k.page = -1;
+    k.off = off;
+    if (pos < k1 && pos >= a.n_sink) {
+      const int pg = __ldg(table + entry);
+      k.page = pg < a.n_pages ? pg : -1;
     }
-    cp_async_commit();
+    pos = min(pos, k1) + kFewWarps * kBlock;
+    entry += a.step_page;
+    off += a.step_off;
+    if (off >= ps) off -= ps, ++entry;
   };
+  const uint32_t page_bytes = static_cast<uint32_t>(a.H * ps) * RB;  // below 2^31
+  const size_t head_at = static_cast<size_t>(h) * ps * RB + kh * (RB / 2);
+  const uint8_t* const kc0 = a.kcodes + head_at;
+  const uint8_t* const vc0 = a.vcodes + head_at;
+  const uint8_t* const z0 = reinterpret_cast<const uint8_t*>((kh ? a.vsz : a.ksz) + static_cast<size_t>(h) * ps * NG);
+  auto issue = [&](uint32_t sb, const Key& k) {  // a block of this warp into the stage at sb
+    const bool live = k.page >= 0;
+    const uint32_t pg = live ? k.page : 0, o = live ? k.off : 0, n = live ? 16u : 0u;
+    const size_t at = static_cast<uint64_t>(pg) * page_bytes + o * static_cast<uint32_t>(RB);
+    const uint32_t to = sb + kt * RB + kh * (RB / 2);
 #pragma unroll
-  for (int i = 0; i < ST; ++i) issue(i, page_of(i));
-  int pn = page_of(ST);
+    for (int c = 0; c < RB / 32; ++c) {
+      cp_async16(to + 16 * c, kc0 + at + 16 * c, n);
+      cp_async16(to + kBlock * RB + 16 * c, vc0 + at + 16 * c, n);
+    }
+    const uint8_t* sz = z0 + static_cast<uint64_t>(pg) * (page_bytes / (RB / (4 * NG))) + o * (4u * NG);
+    const uint32_t zt = sb + 2 * kBlock * RB + (2 * kt + kh) * 4 * NG;
+    if constexpr (NG == 1) cp_async4(zt, sz, live ? 4u : 0u);
+    else if constexpr (NG == 2) cp_async8(zt, sz, live ? 8u : 0u);
+    else cp_async16(zt, sz, n);
+    const uint32_t seen = __ballot_sync(0xffffffffu, live);  // two bits a key
+    if (lane == 0) asm volatile("st.shared.u32 [%0], %1;" ::"r"(sb + 2 * kBlock * (RB + 4 * NG)), "r"(seen) : "memory");
+  };
+  Key next;
+#pragma unroll
+  for (int i = 0; i < ST; ++i) {
+    look_up(next);
+    if (i < mine) issue(wbase + i * C::kStage, next);
+    cp_async_commit();
+  }
+  look_up(next);
 
   // ---- query rows: rotated, scaled by a power of two to [2^13, 2^14)
   for (int r = warp; r < R; r += kFewWarps) {
@@ -844,22 +865,38 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 2 : 1) k_paged_few(cons
     if (lane == 0) qmul[r] = unit * __uint_as_float(static_cast<uint32_t>(127 - 13 + e) << 23) * 16777216.0f;
   }
   __syncthreads();
-  // B fragments of the scores: column gr of tile t is row 4 t + gr / 2, term gr & 1
+  // B fragments of the scores: column gr of tile t is row 4 t + gr / 2, term gr & 1. Each warp makes one k-step.
+  __shared__ uint2 frag[NT][8][32];
+  {
+    constexpr int PK = M::kPairs / 2;  // k-steps of a word
+    uint32_t b2[NT][2];
+#pragma unroll
+    for (int ks = 0; ks < 8; ++ks) {
+      if (ks != warp) continue;
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const float* q = qrow[4 * t + (gr >> 1)];
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          const int p = 2 * (ks % PK) + b, ch = M::kch(ks / PK, p, tig);
+          const float down = 1.0f / static_cast<float>(1 << M::bit(p));
+          b2[t][b] = __byte_perm(hi_lo(q[ch] * down), hi_lo(q[ch + M::kFar] * down), (gr & 1) ? 0x7632 : 0x5410);
+        }
+        frag[t][ks][lane] = make_uint2(b2[t][0], b2[t][1]);
+      }
+    }
+  }
+  __syncthreads();
   uint32_t bq[8][NT][2];
   float mul[NT], qz[NT][NG];
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
-    const float* q = qrow[4 * t + (gr >> 1)];
 #pragma unroll
-    for (int ks = 0; ks < 8; ++ks)
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        constexpr int PK = M::kPairs / 2;  // k-steps of a word
-        const int i = ks / PK, p = 2 * (ks % PK) + b, ch = M::kch(i, p, tig);
-        const float down = 1.0f / static_cast<float>(1 << M::bit(p));
-        const uint32_t x = hi_lo(q[ch] * down), y = hi_lo(q[ch + M::kFar] * down);
-        bq[ks][t][b] = __byte_perm(x, y, (gr & 1) ? 0x7632 : 0x5410);
-      }
+    for (int ks = 0; ks < 8; ++ks) {
+      const uint2 f = frag[t][ks][lane];
+      bq[ks][t][0] = f.x;
+      bq[ks][t][1] = f.y;
+    }
     mul[t] = qmul[4 * t + tig];
 #pragma unroll
     for (int k = 0; k < NG; ++k) qz[t][k] = qsum[4 * t + tig][k];
@@ -886,13 +923,13 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 2 : 1) k_paged_few(cons
   const int srcA = 8 * tig + (gr >> 1), srcB = srcA + 4;
   const uint32_t sel = (gr & 1) ? 0x7632u : 0x5410u;
 
-  for (int i = 0; i < mine; ++i) {
+  uint32_t stage = 0;
+  int n0 = k0 + warp * kBlock;
+  for (int i = 0; i < mine; ++i, n0 += kFewWarps * kBlock) {
     cp_async_wait_group<ST - 1>();
     __syncwarp();
-    const uint8_t* st = wgen + (i % ST) * C::kStage;
-    const uint8_t* kz = st + 2 * kBlock * RB;
-    const uint8_t* vz = kz + kBlock * 4 * NG;
-    const int n0 = k0 + (warp + kFewWarps * i) * kBlock;
+    const uint8_t* st = wgen + stage;
+    const uint8_t* sz = st + 2 * kBlock * RB;  // [key][its groups' (S, Z) of the key, then of the value]
     const uint32_t seen = *reinterpret_cast<const uint32_t*>(st + 2 * kBlock * (RB + 4 * NG));
     // ---- scores of keys gr and gr + 8
     float sc[NG][NT][4];
@@ -921,10 +958,10 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 2 : 1) k_paged_few(cons
     uint32_t ka[NG], kb2[NG], va[NG], vb[NG];
 #pragma unroll
     for (int k = 0; k < NG; ++k) {
-      ka[k] = *reinterpret_cast<const uint32_t*>(kz + (gr * NG + k) * 4);
-      kb2[k] = *reinterpret_cast<const uint32_t*>(kz + ((gr + 8) * NG + k) * 4);
-      va[k] = *reinterpret_cast<const uint32_t*>(vz + (gr * NG + k) * 4);
-      vb[k] = *reinterpret_cast<const uint32_t*>(vz + ((gr + 8) * NG + k) * 4);
+      ka[k] = *reinterpret_cast<const uint32_t*>(sz + (2 * gr * NG + k) * 4);
+      kb2[k] = *reinterpret_cast<const uint32_t*>(sz + (2 * (gr + 8) * NG + k) * 4);
+      va[k] = *reinterpret_cast<const uint32_t*>(sz + ((2 * gr + 1) * NG + k) * 4);
+      vb[k] = *reinterpret_cast<const uint32_t*>(sz + ((2 * (gr + 8) + 1) * NG + k) * 4);
     }
     // log2 of the largest value scale of each key, for the range of its weights
     float ta = kFewMinS, tb = kFewMinS;
@@ -1026,8 +1063,10 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 2 : 1) k_paged_few(cons
       }
     }
     __syncwarp();
-    issue(i + ST, pn);
-    pn = page_of(i + ST + 1);
+    if (i + ST < mine) issue(wbase + stage, next);  // the stage just read
+    cp_async_commit();
+    look_up(next);
+    stage = stage == (ST - 1) * C::kStage ? 0u : stage + C::kStage;
   }
   cp_async_wait_all();
 
@@ -1043,8 +1082,6 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 2 : 1) k_paged_few(cons
     if (gr == 0) {
       wm[warp][4 * t + tig] = mr[t];
       wl[warp][4 * t + tig] = lr[t];
-#pragma unroll
-      for (int k = 0; k < NG; ++k) wz[warp][4 * t + tig][k] = zr[t][k];
     }
   }
   __syncthreads();  // every warp has left its ring: it holds the sums now
@@ -1061,27 +1098,29 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 2 : 1) k_paged_few(cons
 #pragma unroll
       for (int r8 = 0; r8 < 2; ++r8) {
         const float up = 16777216.0f / static_cast<float>(1 << M::bit(M::vcode(mt, r8)));
-        sums[(warp * R + r) * D + M::vch(mt, r8, gr)] = (acc[mt][t][2 * r8] + acc[mt][t][2 * r8 + 1]) * up * f;
+        // the zeros' part is the same for the channels of a group
+        sums[(warp * R + r) * D + M::vch(mt, r8, gr)] =
+            fmaf(acc[mt][t][2 * r8] + acc[mt][t][2 * r8 + 1], up, zr[t][M::vgroup(mt)]) * f;
       }
   }
   __syncthreads();
+  const size_t part = static_cast<size_t>(z) * (static_cast<size_t>(a.n_rows) * a.Hq);
   for (int e = tid; e < n_rows * D; e += kFewThreads) {
     const int r = e / D, ch = e % D;
-    float top = -INFINITY;
+    float o = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kFewWarps; ++w) top = fmaxf(top, wm[w][r]);
-    float o = 0.0f, l = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kFewWarps; ++w) {
-      if (wm[w][r] == -INFINITY && wl[w][r] == 0.0f) continue;
-      const float f = exp2_fast(wm[w][r] - top);
-      o += sums[(w * R + r) * D + ch] + wz[w][r][ch / G] * f;
-      l = fmaf(wl[w][r], f, l);
-    }
-    const size_t at = static_cast<size_t>(z) * (static_cast<size_t>(a.n_rows) * a.Hq) +
-                      (static_cast<size_t>(row0) + r / a.g) * a.Hq + h * a.g + r % a.g;
+    for (int w = 0; w < kFewWarps; ++w) o += sums[(w * R + r) * D + ch];
+    const size_t at = part + (static_cast<size_t>(row0) + r / a.g) * a.Hq + h * a.g + r % a.g;
     a.part_o[at * D + tile_pos<BITS>(ch)] = o;
-    if (ch == 0) a.part_s[at] = make_float2(top - kFewUp, l);
+  }
+  if (tid < n_rows) {
+    float top = -INFINITY, l = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kFewWarps; ++w) top = fmaxf(top, wm[w][tid]);
+#pragma unroll
+    for (int w = 0; w < kFewWarps; ++w)
+      if (wl[w][tid] != 0.0f) l = fmaf(wl[w][tid], exp2_fast(wm[w][tid] - top), l);
+    a.part_s[part + (static_cast<size_t>(row0) + tid / a.g) * a.Hq + h * a.g + tid % a.g] = make_float2(top - kFewUp, l);
   }
 }
 
@@ -1096,15 +1135,17 @@ Plan make_plan(const kvq_desc& d, int q_heads, int n_seqs, int n_rows, int max_r
   Plan p{};
   const int g = q_heads / heads;
   p.T = 128 / g;
-  p.few = d.head_dim == 128 && d.bits != 3 && static_cast<long long>(max_rows) * g <= 8;
+  p.few = d.head_dim == 128 && d.bits != 3 && static_cast<long long>(max_rows) * g <= 8 &&
+          static_cast<long long>(d.heads) * d.t_cap * 64 < (1ll << 31);  // a page's codes in 32 bits
   p.shared = max_rows > p.T;
   const long long tt = p.shared ? 2 * p.T : p.T;
   const long long by_rows = n_rows / tt + n_seqs, by_max = n_seqs * ((max_rows + tt - 1) / tt);
   p.tiles = p.few ? n_seqs : by_rows < by_max ? by_rows : by_max;
   // about four CTAs per SM of 148 in turn, of at least 1024 keys each
   const long long all = p.tiles * heads, keys = max_kv > 0 ? max_kv : 1;
-  long long n = all > 0 ? 4 * 148 / all : 1;
-  const long long most = (keys + 1023) / 1024;
+  const long long tgt = getenv("TGT") ? atoi(getenv("TGT")) : 592, mk = getenv("MINK") ? atoi(getenv("MINK")) : 1024;
+  long long n = all > 0 ? tgt / all : 1;
+  const long long most = (keys + mk - 1) / mk;
   n = n < 1 ? 1 : n > most ? most : n;
   if (n > 256) n = 256;
   long long len = (keys + n - 1) / n;
@@ -1192,6 +1233,8 @@ kvq_status launch_attend_paged(const kvq_desc& dk, const kvq_desc&, const void* 
   a.n_stretch = p.n_stretch;
   a.n_parts = p.n_parts;
   a.div_ps = FastDiv(static_cast<uint32_t>(dk.t_cap));
+  a.step_page = 128 / dk.t_cap;
+  a.step_off = 128 % dk.t_cap;
   a.q_stride = q_stride;
   a.out_stride = out_stride;
   a.scale = scale;

@@ -177,16 +177,18 @@ __global__ void __launch_bounds__(kMapThreads) k_page_map(const MapArgs a) {
 }
 
 // ---------------------------------------------------------------- rows
-// D / 16 lanes hold a row of one head, 16 consecutive channels each: a lane
-// loads 32 contiguous bytes, a warp 1 KB. FWHT strides 1 .. 8 run in registers
-// on packed pairs, strides 16 .. D/2 by shuffle (every lane computes
-// fma(own, +-1, partner): exactly a + b below and a - b above). Rows go
-// head-fastest, so the heads of a token share its (cos, sin) row in L1.
+// L = D / 16 lanes hold a row of one head; lane p has channels 8p .. 8p+7 and
+// the same of the upper half, so each half of a row is one run of 16-byte loads
+// and both RoPE pairings stay inside a lane. P[i] = (x[8p + i], x[D/2 + 8p + i]).
+// FWHT strides in ascending order: 1, 2, 4 on packed pairs, 8 .. D/4 by shuffle
+// (every lane computes fma(own, +-1, partner): exactly a + b below and a - b
+// above), D/2 inside the pairs. Rows go head-fastest, so the heads of a token
+// share its (cos, sin) row in L1.
 constexpr int kRowThreads = 256;
-constexpr int kC = 16;  // channels per lane
 
 struct RowArgs {
-  int H, n_sink, rope, rope_rows, rot, lpg, sink_rows, out_fp32;
+  int H, n_sink, rope, rope_rows, rot, sink_rows, out_fp32;
+  int whole, lanes;  // a group is the whole row; else the lanes of a group within a half
   uint32_t n_vec;  // n_rows * H
   int64_t stride;  // elements between the rows of x / out
   FastDiv div_h, div_ps;
@@ -234,75 +236,122 @@ __device__ __forceinline__ RowPlace place(const RowArgs& a, uint32_t v) {
   return p;
 }
 
-// (cos, sin) of this lane's channels: mode 1 (pairs 2i, 2i+1) 8 pairs, mode 2
-// (pairs i, i + D/2) the 16 angles of its channels modulo D/2.
+// RoPE of both pairings, in the fma order of rope_fwd.
 template <int D, bool INV>
-__device__ __forceinline__ void rope_rows16(const RowArgs& a, int m, int part, float (&x)[kC]) {
-  constexpr int L = D / kC;
+__device__ __forceinline__ void rope_row(const RowArgs& a, int m, int part, float2 (&P)[8]) {
   const float4* cs = reinterpret_cast<const float4*>(a.rope_cs + static_cast<size_t>(m) * D);
-  if (a.rope == 1) {
+  if (a.rope == 1) {  // pairs 4p .. 4p+3 of each half
 #pragma unroll
-    for (int i = 0; i < kC / 4; ++i) {
-      const float4 c = __ldg(cs + part * (kC / 4) + i);
-      float x0 = x[4 * i], x1 = x[4 * i + 1], x2 = x[4 * i + 2], x3 = x[4 * i + 3];
-      rope_fwd(x0, x1, c.x, INV ? -c.y : c.y);
-      rope_fwd(x2, x3, c.z, INV ? -c.w : c.w);
-      x[4 * i] = x0, x[4 * i + 1] = x1, x[4 * i + 2] = x2, x[4 * i + 3] = x3;
-    }
-  } else {
-    const bool up = part >= L / 2;
-#pragma unroll
-    for (int i = 0; i < kC / 2; ++i) {
-      const float4 c = __ldg(cs + (part & (L / 2 - 1)) * (kC / 2) + i);
+    for (int i = 0; i < 2; ++i) {
+      const float4 u = __ldg(cs + 2 * part + i), v = __ldg(cs + D / 8 + 2 * part + i);
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const float own = x[2 * i + e];
-        const float oth = __shfl_xor_sync(0xffffffffu, own, L / 2);
-        float x0 = up ? oth : own, x1 = up ? own : oth;
-        rope_fwd(x0, x1, e ? c.z : c.x, INV ? -(e ? c.w : c.y) : (e ? c.w : c.y));
-        x[2 * i + e] = up ? x1 : x0;
+        const float2 c = e ? f2(u.z, v.z) : f2(u.x, v.x), t = e ? f2(u.w, v.w) : f2(u.y, v.y), n = f2(-t.x, -t.y);
+        const float2 x0 = P[4 * i + 2 * e], x1 = P[4 * i + 2 * e + 1];
+        P[4 * i + 2 * e] = fma2(x0, c, mul2(x1, INV ? t : n));
+        P[4 * i + 2 * e + 1] = fma2(x0, INV ? n : t, mul2(x1, c));
       }
+    }
+  } else {  // pairs (i, i + D/2), angles 8p .. 8p+7
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 u = __ldg(cs + 4 * part + i);
+      rope_fwd(P[2 * i].x, P[2 * i].y, u.x, INV ? -u.y : u.y);
+      rope_fwd(P[2 * i + 1].x, P[2 * i + 1].y, u.z, INV ? -u.w : u.w);
     }
   }
 }
 
-// Unnormalised FWHT of a row held by D / 16 lanes.
+// Unnormalised FWHT of a row.
 template <int D>
-__device__ __forceinline__ void fwht_rows16(int part, float (&x)[kC]) {
-  float2 P[kC / 2];  // the register-pair layout of fwht_pairs
+__device__ __forceinline__ void fwht_row(int part, float2 (&P)[8]) {
 #pragma unroll
-  for (int g = 0; g < kC / 4; ++g) {
-    P[2 * g] = f2(x[4 * g], x[4 * g + 2]);
-    P[2 * g + 1] = f2(x[4 * g + 1], x[4 * g + 3]);
-  }
-  fwht_pairs<kC>(P);
+  for (int h = 1; h < 8; h <<= 1)
 #pragma unroll
-  for (int o = 1; o < D / kC; o <<= 1) {
+    for (int i = 0; i < 8; ++i)
+      if ((i & h) == 0) bfly(P[i], P[i + h]);
+#pragma unroll
+  for (int o = 1; o < D / 16; o <<= 1) {
     const float sg = (part & o) ? -1.0f : 1.0f;
 #pragma unroll
-    for (int k = 0; k < kC / 2; ++k) {
+    for (int k = 0; k < 8; ++k) {
       const float2 q = f2(__shfl_xor_sync(0xffffffffu, P[k].x, o), __shfl_xor_sync(0xffffffffu, P[k].y, o));
       P[k] = fma2(P[k], f2(sg, sg), q);
     }
   }
 #pragma unroll
-  for (int g = 0; g < kC / 4; ++g) {
-    x[4 * g] = P[2 * g].x;
-    x[4 * g + 2] = P[2 * g].y;
-    x[4 * g + 1] = P[2 * g + 1].x;
-    x[4 * g + 3] = P[2 * g + 1].y;
+  for (int k = 0; k < 8; ++k) P[k] = f2(__fadd_rn(P[k].x, P[k].y), __fsub_rn(P[k].x, P[k].y));
+}
+
+// Rows of the permutation in shared memory: channel j at j + 4 (j / 32), so that the lanes' 16-byte
+// accesses (32 bytes apart) meet different banks.
+__device__ __forceinline__ int row_at(int j) { return j + ((j >> 5) << 2); }
+template <int D>
+__host__ __device__ constexpr int row_words() { return D + D / 8; }
+template <int D>
+constexpr size_t perm_smem() { return static_cast<size_t>(kRowThreads / 32) * (512 / D) * row_words<D>() * 4; }
+
+// Own channels of a row into the buffer / out of it.
+template <int D>
+__device__ __forceinline__ void put_own(float* buf, int part, const float2 (&P)[8]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    *reinterpret_cast<float4*>(buf + row_at(8 * part + 4 * i)) = make_float4(P[4 * i].x, P[4 * i + 1].x, P[4 * i + 2].x, P[4 * i + 3].x);
+    *reinterpret_cast<float4*>(buf + row_at(D / 2 + 8 * part + 4 * i)) = make_float4(P[4 * i].y, P[4 * i + 1].y, P[4 * i + 2].y, P[4 * i + 3].y);
+  }
+}
+template <int D>
+__device__ __forceinline__ void get_own(const float* buf, int part, float2 (&P)[8]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float4 u = *reinterpret_cast<const float4*>(buf + row_at(8 * part + 4 * i));
+    const float4 v = *reinterpret_cast<const float4*>(buf + row_at(D / 2 + 8 * part + 4 * i));
+    P[4 * i] = f2(u.x, v.x), P[4 * i + 1] = f2(u.y, v.y), P[4 * i + 2] = f2(u.z, v.z), P[4 * i + 3] = f2(u.w, v.w);
+  }
+}
+// perm[h][own channels], low and high halves of words in channel order.
+template <int D>
+__device__ __forceinline__ void own_perm(const RowArgs& a, int h, int part, uint4& lo, uint4& hi) {
+  const uint4* pr = reinterpret_cast<const uint4*>(a.perm + static_cast<size_t>(h) * D) + part;
+  lo = __ldg(pr);
+  hi = __ldg(pr + D / 16);
+}
+__device__ __forceinline__ int nth16(const uint4& v, int i) {
+  const uint32_t w = i < 2 ? v.x : i < 4 ? v.y : i < 6 ? v.z : v.w;
+  return static_cast<int>((w >> (16 * (i & 1))) & 0xffffu);
+}
+
+// The eight codes of one half of a lane, BITS each, to and from the record. Three bits: four lanes'
+// 24-bit runs are three words, which the first three of them hold.
+template <int BITS>
+__device__ __forceinline__ void store_codes(uint8_t* at, int part, uint32_t w, bool live) {
+  if constexpr (BITS == 2) {
+    if (live) *reinterpret_cast<uint16_t*>(at + 2 * part) = static_cast<uint16_t>(w);
+  } else if constexpr (BITS == 4) {
+    if (live) *reinterpret_cast<uint32_t*>(at + 4 * part) = w;
+  } else {
+    const int k = part & 3;
+    const uint32_t up = __shfl_down_sync(0xffffffffu, w, 1);
+    if (live && k < 3) *reinterpret_cast<uint32_t*>(at + 12 * (part >> 2) + 4 * k) = (w >> (8 * k)) | (up << (24 - 8 * k));
+  }
+}
+template <int BITS>
+__device__ __forceinline__ uint32_t load_codes(const uint8_t* at, int part) {
+  if constexpr (BITS == 2) {
+    return __ldg(reinterpret_cast<const uint16_t*>(at + 2 * part));
+  } else if constexpr (BITS == 4) {
+    return __ldg(reinterpret_cast<const uint32_t*>(at + 4 * part));
+  } else {
+    const int k = part & 3;
+    const uint32_t own = k < 3 ? __ldg(reinterpret_cast<const uint32_t*>(at + 12 * (part >> 2) + 4 * k)) : 0u;
+    const uint32_t before = __shfl_up_sync(0xffffffffu, own, 1);
+    return k == 0 ? own : __funnelshift_r(before, own, 32 - 8 * k);
   }
 }
 
-// A warp's rows of the permutation: D floats and four of padding each.
-template <int D>
-__host__ __device__ constexpr int row_words() { return D + 4; }
-template <int D>
-constexpr size_t perm_smem() { return static_cast<size_t>(kRowThreads / 32) * (32 * kC / D) * row_words<D>() * 4; }
-
 template <int D, int BITS>
 __global__ void __launch_bounds__(kRowThreads) k_encode_rows(const RowArgs a) {
-  constexpr int L = D / kC, VW = 32 / L;  // lanes per row, rows per warp
+  constexpr int L = D / 16, VW = 32 / L;  // lanes per row, rows per warp
   constexpr int RB = D * BITS / 8;
   extern __shared__ __align__(16) float row_smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = lane % L;
@@ -310,129 +359,149 @@ __global__ void __launch_bounds__(kRowThreads) k_encode_rows(const RowArgs a) {
   const uint32_t step = gridDim.x * (kRowThreads / 32) * VW;
   for (uint32_t base = (blockIdx.x * (kRowThreads / 32) + warp) * VW; base < a.n_vec; base += step) {
     const RowPlace p = place<D>(a, base + lane / L);
-    const uint4* src = reinterpret_cast<const uint4*>(a.x + static_cast<int64_t>(p.row) * a.stride + p.h * D + part * kC);
-    const uint4 r0 = __ldg(src), r1 = __ldg(src + 1);
-    float x[kC];
-    h8_to_f32(r0, x);
-    h8_to_f32(r1, x + 8);
-    if (p.sink) {
-      uint4* dst = reinterpret_cast<uint4*>(a.sink + p.sink_at + part * kC);
-      dst[0] = r0;
-      dst[1] = r1;
+    const uint4* src = reinterpret_cast<const uint4*>(a.x + static_cast<int64_t>(p.row) * a.stride + p.h * D) + part;
+    const uint4 r0 = __ldg(src), r1 = __ldg(src + D / 16);
+    float2 P[8];
+    {
+      float lo[8], hi[8];
+      h8_to_f32(r0, lo);
+      h8_to_f32(r1, hi);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) P[i] = f2(lo[i], hi[i]);
     }
-    if (a.rope) rope_rows16<D, false>(a, p.m, part, x);
-    if (a.perm) {
-#pragma unroll
-      for (int i = 0; i < kC / 4; ++i)
-        reinterpret_cast<float4*>(buf + part * kC)[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+    if (p.sink) {
+      uint4* dst = reinterpret_cast<uint4*>(a.sink + p.sink_at) + part;
+      dst[0] = r0;
+      dst[D / 16] = r1;
+    }
+    if (a.rope) rope_row<D, false>(a, p.m, part, P);
+    if (a.perm) {  // p_j = y[perm[j]]
+      uint4 lo, hi;
+      own_perm<D>(a, p.h, part, lo, hi);
+      put_own<D>(buf, part, P);
       __syncwarp();
-      const uint4* pr = reinterpret_cast<const uint4*>(a.perm + static_cast<size_t>(p.h) * D + part * kC);
-      const uint4 p0 = __ldg(pr), p1 = __ldg(pr + 1);
-      const uint32_t pw[8] = {p0.x, p0.y, p0.z, p0.w, p1.x, p1.y, p1.z, p1.w};
 #pragma unroll
-      for (int i = 0; i < kC; ++i) x[i] = buf[(pw[i >> 1] >> (16 * (i & 1))) & (D - 1)];
+      for (int i = 0; i < 8; ++i)
+        P[i] = f2(buf[row_at(nth16(lo, i) & (D - 1))], buf[row_at(nth16(hi, i) & (D - 1))]);
       __syncwarp();
     }
     if (a.rot) {
-      fwht_rows16<D>(part, x);
+      fwht_row<D>(part, P);
 #pragma unroll
-      for (int i = 0; i < kC; ++i) x[i] = __fmul_rn(x[i], a.rscale);
+      for (int i = 0; i < 8; ++i) P[i] = mul2(P[i], f2(a.rscale, a.rscale));
     }
-    float lo = x[0], hi = x[0];
+    // the halves' ranges, joined where a group is the whole row
+    float2 mn = P[0], mx = P[0];
 #pragma unroll
-    for (int i = 1; i < kC; ++i) lo = fminf(lo, x[i]), hi = fmaxf(hi, x[i]);
+    for (int i = 1; i < 8; ++i) {
+      mn = f2(fminf(mn.x, P[i].x), fminf(mn.y, P[i].y));
+      mx = f2(fmaxf(mx.x, P[i].x), fmaxf(mx.y, P[i].y));
+    }
+    if (a.whole) {
+      mn.x = fminf(mn.x, mn.y);
+      mx.x = fmaxf(mx.x, mx.y);
+    }
 #pragma unroll
     for (int o = 1; o < L; o <<= 1)
-      if (o < a.lpg) {
-        lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+      if (o < a.lanes) {
+        mn.x = fminf(mn.x, __shfl_xor_sync(0xffffffffu, mn.x, o));
+        mx.x = fmaxf(mx.x, __shfl_xor_sync(0xffffffffu, mx.x, o));
+        if (!a.whole) {
+          mn.y = fminf(mn.y, __shfl_xor_sync(0xffffffffu, mn.y, o));
+          mx.y = fmaxf(mx.y, __shfl_xor_sync(0xffffffffu, mx.y, o));
+        }
       }
-    QParams q = minmax_params<BITS>(lo, hi);
-    if (p.sink) {
-      q.Z = q.R = 0.0f;
-      q.sz = __halves2half2(__ushort_as_half(0), __ushort_as_half(0));
+    QParams q0 = minmax_params<BITS>(mn.x, mx.x), q1 = a.whole ? q0 : minmax_params<BITS>(mn.y, mx.y);
+    if (p.sink) {  // a sink's record is zero: every value quantizes with Z = R = 0
+      q0.Z = q0.R = q1.Z = q1.R = 0.0f;
+      q0.sz = q1.sz = __halves2half2(__ushort_as_half(0), __ushort_as_half(0));
     }
-    uint64_t w = 0;  // 16 codes: 4, 6 or 8 bytes
+    // code = the integer added to the magic constant; its pattern's offset is taken off once per word
+    uint32_t w0 = 0, w1 = 0;
 #pragma unroll
-    for (int i = 0; i < kC; ++i) {
-      const float u = __fmaf_rn(__fsub_rn(x[i], q.Z), q.R, kMagicRound);
-      // a NaN or overflowed group has no code: whatever bits it gives stay in its own field
-      const uint32_t c = (__float_as_uint(u) - kMagicBits) & ((1u << BITS) - 1u);
-      w |= static_cast<uint64_t>(p.sink ? 0u : c) << (BITS * i);
+    for (int i = 0; i < 8; ++i) {
+      const float2 u = fma2(add2(P[i], f2(-q0.Z, -q1.Z)), f2(q0.R, q1.R), f2(kMagicRound, kMagicRound));
+      w0 += __float_as_uint(u.x) << (BITS * i);
+      w1 += __float_as_uint(u.y) << (BITS * i);
     }
+    w0 -= magic_offset<BITS, 8>();
+    w1 -= magic_offset<BITS, 8>();
+    if constexpr (BITS == 3) w0 &= 0xffffffu, w1 &= 0xffffffu;
+    uint8_t* dst = a.codes + p.rec * RB;
+    store_codes<BITS>(dst, part, w0, p.live);
+    store_codes<BITS>(dst + RB / 2, part, w1, p.live);
     if (p.live) {
-      uint8_t* dst = a.codes + p.rec * RB + part * (kC * BITS / 8);
-      if constexpr (BITS == 2) {
-        *reinterpret_cast<uint32_t*>(dst) = static_cast<uint32_t>(w);
-      } else if constexpr (BITS == 4) {
-        *reinterpret_cast<uint2*>(dst) = make_uint2(static_cast<uint32_t>(w), static_cast<uint32_t>(w >> 32));
-      } else {
-#pragma unroll
-        for (int i = 0; i < 3; ++i) reinterpret_cast<uint16_t*>(dst)[i] = static_cast<uint16_t>(w >> (16 * i));
+      if (a.whole) {
+        if (part == 0) a.sz[p.rec] = q0.sz;
+      } else if (part % a.lanes == 0) {  // groups of the lower half, then of the upper
+        const int per = L / a.lanes;
+        __half2* z = a.sz + p.rec * (2 * per) + part / a.lanes;
+        z[0] = q0.sz;
+        z[per] = q1.sz;
       }
-      if (part % a.lpg == 0) a.sz[p.rec * (L / a.lpg) + part / a.lpg] = q.sz;
     }
   }
 }
 
 template <int D, int BITS>
 __global__ void __launch_bounds__(kRowThreads) k_decode_rows(const RowArgs a) {
-  constexpr int L = D / kC, VW = 32 / L;
+  constexpr int L = D / 16, VW = 32 / L;
   constexpr int RB = D * BITS / 8;
+  constexpr uint32_t MASK = (1u << BITS) - 1u;
   extern __shared__ __align__(16) float row_smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = lane % L;
   float* buf = row_smem + (warp * VW + lane / L) * row_words<D>();
   const uint32_t step = gridDim.x * (kRowThreads / 32) * VW;
   for (uint32_t base = (blockIdx.x * (kRowThreads / 32) + warp) * VW; base < a.n_vec; base += step) {
     const RowPlace p = place<D>(a, base + lane / L);
-    const uint8_t* src = a.codes + p.rec * RB + part * (kC * BITS / 8);
-    uint64_t w;
-    if constexpr (BITS == 2) {
-      w = __ldg(reinterpret_cast<const uint32_t*>(src));
-    } else if constexpr (BITS == 4) {
-      const uint2 u = __ldg(reinterpret_cast<const uint2*>(src));
-      w = u.x | (static_cast<uint64_t>(u.y) << 32);
-    } else {
-      const uint16_t* h = reinterpret_cast<const uint16_t*>(src);
-      w = __ldg(h) | (static_cast<uint64_t>(__ldg(h + 1)) << 16) | (static_cast<uint64_t>(__ldg(h + 2)) << 32);
+    const uint8_t* src = a.codes + p.rec * RB;
+    const uint32_t w0 = load_codes<BITS>(src, part), w1 = load_codes<BITS>(src + RB / 2, part);
+    const int per = a.whole ? 0 : L / a.lanes;
+    const __half2* z = a.sz + (a.whole ? p.rec : p.rec * (2 * per) + part / a.lanes);
+    float2 s0 = __half22float2(z[0]), s1 = __half22float2(z[per]);
+    if (a.rot) s0 = mul2(s0, f2(a.rscale, a.rscale)), s1 = mul2(s1, f2(a.rscale, a.rscale));
+    float2 P[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float2 c = f2(__uint_as_float(0x4B000000u | ((w0 >> (BITS * i)) & MASK)),
+                          __uint_as_float(0x4B000000u | ((w1 >> (BITS * i)) & MASK)));
+      P[i] = fma2(add2(c, f2(-8388608.0f, -8388608.0f)), f2(s0.x, s1.x), f2(s0.y, s1.y));
     }
-    const float2 sz = __half22float2(a.sz[p.rec * (L / a.lpg) + part / a.lpg]);
-    const float S = a.rot ? __fmul_rn(sz.x, a.rscale) : sz.x, Z = a.rot ? __fmul_rn(sz.y, a.rscale) : sz.y;
-    float x[kC];
-#pragma unroll
-    for (int i = 0; i < kC; ++i)
-      x[i] = __fmaf_rn(code_to_float(static_cast<uint32_t>(w >> (BITS * i)) & ((1u << BITS) - 1u)), S, Z);
-    if (a.rot) fwht_rows16<D>(part, x);
+    if (a.rot) fwht_row<D>(part, P);
     if (a.perm) {  // x[perm[j]] = p_j
-      const uint4* pr = reinterpret_cast<const uint4*>(a.perm + static_cast<size_t>(p.h) * D + part * kC);
-      const uint4 p0 = __ldg(pr), p1 = __ldg(pr + 1);
-      const uint32_t pw[8] = {p0.x, p0.y, p0.z, p0.w, p1.x, p1.y, p1.z, p1.w};
+      uint4 lo, hi;
+      own_perm<D>(a, p.h, part, lo, hi);
 #pragma unroll
-      for (int i = 0; i < kC; ++i) buf[(pw[i >> 1] >> (16 * (i & 1))) & (D - 1)] = x[i];
-      __syncwarp();
-#pragma unroll
-      for (int i = 0; i < kC / 4; ++i) {
-        const float4 f = reinterpret_cast<const float4*>(buf + part * kC)[i];
-        x[4 * i] = f.x, x[4 * i + 1] = f.y, x[4 * i + 2] = f.z, x[4 * i + 3] = f.w;
+      for (int i = 0; i < 8; ++i) {
+        buf[row_at(nth16(lo, i) & (D - 1))] = P[i].x;
+        buf[row_at(nth16(hi, i) & (D - 1))] = P[i].y;
       }
       __syncwarp();
+      get_own<D>(buf, part, P);
+      __syncwarp();
     }
-    if (a.rope) rope_rows16<D, true>(a, p.m, part, x);
+    if (a.rope) rope_row<D, true>(a, p.m, part, P);
+    float lo[8], hi[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) lo[i] = P[i].x, hi[i] = P[i].y;
     if (p.sink) {
-      const uint4* s = reinterpret_cast<const uint4*>(a.sink + p.sink_at + part * kC);
-      h8_to_f32(s[0], x);
-      h8_to_f32(s[1], x + 8);
+      const uint4* s = reinterpret_cast<const uint4*>(a.sink + p.sink_at) + part;
+      h8_to_f32(s[0], lo);
+      h8_to_f32(s[D / 16], hi);
     }
     if (p.live) {
-      const int64_t at = static_cast<int64_t>(p.row) * a.stride + p.h * D + part * kC;
+      const int64_t at = static_cast<int64_t>(p.row) * a.stride + p.h * D + 8 * part;
       if (a.out_fp32) {
         float4* o = reinterpret_cast<float4*>(static_cast<float*>(a.out) + at);
+        float4* o2 = reinterpret_cast<float4*>(static_cast<float*>(a.out) + at + D / 2);
 #pragma unroll
-        for (int i = 0; i < kC / 4; ++i) o[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+        for (int i = 0; i < 2; ++i) {
+          o[i] = make_float4(lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
+          o2[i] = make_float4(hi[4 * i], hi[4 * i + 1], hi[4 * i + 2], hi[4 * i + 3]);
+        }
       } else {
-        uint4* o = reinterpret_cast<uint4*>(static_cast<__half*>(a.out) + at);
-        o[0] = f32_to_h8(x);
-        o[1] = f32_to_h8(x + 8);
+        *reinterpret_cast<uint4*>(static_cast<__half*>(a.out) + at) = f32_to_h8(lo);
+        *reinterpret_cast<uint4*>(static_cast<__half*>(a.out) + at + D / 2) = f32_to_h8(hi);
       }
     }
   }
@@ -444,7 +513,7 @@ kvq_status run_rows(bool enc, const RowArgs& a, const LaunchCtx& ctx, cudaStream
                        : reinterpret_cast<const void*>(k_decode_rows<D, BITS>);
   const size_t smem = a.perm ? perm_smem<D>() : 0;
   const int per_sm = occupancy_once(fn, kRowThreads, smem);
-  const long long per_cta = (kRowThreads / 32) * (32 * kC / D);
+  const long long per_cta = (kRowThreads / 32) * (512 / D);
   const long long steps = (static_cast<long long>(a.n_vec) + per_cta - 1) / per_cta;
   const long long want = static_cast<long long>(ctx.num_sms) * per_sm;
   const unsigned grid = static_cast<unsigned>(steps < want ? steps : want);
@@ -463,7 +532,8 @@ kvq_status launch_rows(bool enc, const kvq_desc& d, const kvq_paged& pg, const k
   a.rope = d.rope;
   a.rope_rows = tb.rope_rows;
   a.rot = d.rot == KVQ_ROT_FWHT_HEAD;
-  a.lpg = d.group / kC;
+  a.whole = d.group == d.head_dim;
+  a.lanes = a.whole ? d.head_dim / 16 : d.group / 8;
   a.sink_rows = pg.sink_rows;
   a.out_fp32 = out_fp32;
   a.n_vec = static_cast<uint32_t>(pg.n_rows) * static_cast<uint32_t>(d.heads);

@@ -461,12 +461,20 @@ def _rows(t: torch.Tensor, name: str, dtypes, heads=None, dim=None) -> int:
 
 def _call(name: str, args: tuple, keep: tuple, stream):
     """A zero-argument call of the entry point `name`: on `stream`, or on the stream that is current
-    when it is called (so a bound call can be captured)."""
-    from . import lib
-    fn, keep_stream = getattr(lib, name), None if stream is None else _stream(stream)
+    when it is called (so a bound call can be captured). The arguments are converted here, once: the
+    call costs the library's own time and about 2 us."""
+    from . import KVQ_OK, lib
+    types = getattr(lib, name).argtypes
+    fn = lib[name]  # a handle without argtypes: the converted arguments pass as they are
+    fn.restype = ctypes.c_int32
+    args = tuple(t(a) if isinstance(a, (int, float)) else a for t, a in zip(types, args))
+    fixed = None if stream is None else ctypes.c_void_p(_stream(stream))
+    dev = torch.cuda.current_device()
 
     def call():
-        check(fn(*args, _stream(None) if keep_stream is None else keep_stream), name)
+        status = fn(*args, fixed if fixed is not None else ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(dev)))
+        if status != KVQ_OK:
+            check(status, name)
     call.keep = keep
     return call
 
