@@ -7,8 +7,8 @@
 //
 // k_paged_tiles: a CTA takes a tile of query rows of one KV head (row t * g +
 // j is token t, query head j of the group of g) and a stretch of its keys, in
-// tiles of 128. Eight warps turn records into fp16 tiles in shared memory (read
-// through the block table, a thread per half record), one thread issues the
+// tiles of 128. A warpgroup turns records into fp16 tiles in shared memory (read
+// through the block table, a thread per record), one thread issues the
 // products, and a warpgroup per slot does the softmax (kvq_flash.cuh). The two
 // slots are two tiles of 128 rows that share every tile of keys (a chunk of a
 // prompt: SHARED), or the same rows with alternate tiles of keys (up to 128 rows,
@@ -17,7 +17,6 @@
 // k_paged_merge: one warp per row and query head joins them with the sinks and
 // turns the result back.
 #include <math.h>
-#include <stdlib.h>
 
 #include "kvq_flash.cuh"
 #include "kvq_internal.h"
@@ -25,14 +24,18 @@
 namespace kvq {
 namespace {
 
-constexpr int kProdWarps = 8;
-constexpr int kThreads = 32 * (8 + kProdWarps + 1);  // softmax 0-7, records 8-15, products 16
+constexpr int kProdWarps = 4;
+constexpr int kThreads = 512;  // warps 0-7 softmax, 8-11 records, 12 products, the rest idle
+// Registers a thread has at launch (the launch bound's limit), and after the split by warpgroup. A sum
+// above the launch's would wait for ever.
+constexpr int kRegsLaunch = 128, kRegsSoftmax = 200, kRegsRecords = 88, kRegsIssue = 24;
+static_assert(256 * kRegsSoftmax + 128 * kRegsRecords + 128 * kRegsIssue <= kThreads * kRegsLaunch, "register split");
 constexpr int kMasks = 8;  // key masks kept: more tiles than are in flight
 
 struct PagedArgs {
   int S, n_rows, max_pages, sink_rows, H, Hq, g, T, n_pages, n_sink, rope, rope_rows, rot, max_rows;
   int stretch, n_stretch, n_parts;  // keys of a CTA, CTAs along the keys, partial results per row
-  int step_page, step_off;          // 128 keys in pages and a rest
+  int step_page, step_off;          // kFewStep keys in pages and a rest
   FastDiv div_ps;
   int64_t q_stride, out_stride;
   float scale, rscale;
@@ -127,67 +130,52 @@ struct Unit<3> {
   }
 };
 
-// Half a record in registers.
+// A record in registers.
 template <int D, int BITS, int G>
-struct Half {
-  static constexpr int kCh = D / 2, kWords = kCh * BITS / 32, kSz = G >= kCh ? 1 : kCh / G;
+struct Record {
+  static constexpr int kWords = D * BITS / 32, kSz = D / G;
   uint32_t w[kWords], sz[kSz];
-  __device__ __forceinline__ void clear() {
+  __device__ __forceinline__ void load(const uint8_t* codes, const __half2* s, size_t rec, bool live) {
+    if (!live) {
 #pragma unroll
-    for (int i = 0; i < kWords; ++i) w[i] = 0;
+      for (int i = 0; i < kWords; ++i) w[i] = 0;
 #pragma unroll
-    for (int i = 0; i < kSz; ++i) sz[i] = 0;
-  }
-  __device__ __forceinline__ void load(const uint8_t* codes, const __half2* s, size_t rec, int half) {
-    const uint8_t* p = codes + rec * (D * BITS / 8) + half * (4 * kWords);
+      for (int i = 0; i < kSz; ++i) sz[i] = 0;
+      return;
+    }
+    const uint8_t* p = codes + rec * (4 * kWords);
     if constexpr (kWords % 4 == 0) {
 #pragma unroll
       for (int i = 0; i < kWords / 4; ++i) {
         const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + i);
         w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
       }
-    } else if constexpr (kWords % 2 == 0) {
+    } else {
 #pragma unroll
       for (int i = 0; i < kWords / 2; ++i) {
         const uint2 v = __ldg(reinterpret_cast<const uint2*>(p) + i);
         w[2 * i] = v.x, w[2 * i + 1] = v.y;
       }
-    } else {
-#pragma unroll
-      for (int i = 0; i < kWords; ++i) w[i] = __ldg(reinterpret_cast<const uint32_t*>(p) + i);
     }
-    const uint32_t* z = reinterpret_cast<const uint32_t*>(s) + rec * (D / G) + (G >= D ? 0 : half * kSz);
+    const uint32_t* z = reinterpret_cast<const uint32_t*>(s) + rec * kSz;
 #pragma unroll
     for (int i = 0; i < kSz; ++i) sz[i] = __ldg(z + i);
   }
-  // Row r of a tile: this half's channels as fp16. The two halves of a record write the 16-byte
-  // chunks in an order four apart, so the 8 lanes of a store phase meet 8 different bank groups.
-  __device__ __forceinline__ void store(uint32_t tile, int r, int half) const {
+  // Row r of a tile as fp16: the eight lanes of a store phase have eight rows, so the swizzle sends
+  // them to eight bank groups.
+  __device__ __forceinline__ void store(uint32_t tile, int r) const {
     using U = Unit<BITS>;
     constexpr int UC = 2 * U::kPairs;  // channels of a unit
-    constexpr int UW = U::kWords;
-    constexpr int NU = kCh / UC;
-    constexpr int TB = D == 128 ? 1 : 0;  // D = 64: both halves in one 128-byte row
-    const uint32_t row = tile + (TB ? half * kTileBytes : 0) + r * 128u;
-    const int x = (r & 7) ^ (TB ? half * 4 : 0);
+    const uint32_t row = tile + r * 128u, x = static_cast<uint32_t>(r & 7) << 4;
 #pragma unroll
-    for (int u = 0; u < NU; ++u) {
-      // the unit that goes to the chunks of u, with the halves' order swapped
-      uint32_t in[UW];
-      constexpr int SW = NU >= 2 && TB ? NU / 2 : 0;
-#pragma unroll
-      for (int i = 0; i < UW; ++i) in[i] = SW ? (half ? w[((u + SW) % NU) * UW + i] : w[u * UW + i]) : w[u * UW + i];
-      const uint32_t sa = sz[kSz == 1 ? 0 : u * UC / G], sb = sz[kSz == 1 ? 0 : ((u + SW) % NU) * UC / G];
-      const uint32_t s = SW && half ? sb : sa;
-      const uint32_t S = __byte_perm(s, s, 0x1010), Z = __byte_perm(s, s, 0x3232);
+    for (int u = 0; u < D / UC; ++u) {
+      const uint32_t s = sz[u * UC / G];
       uint32_t o[U::kPairs];
-      U::open(in, S, Z, o);
+      U::open(w + u * U::kWords, __byte_perm(s, s, 0x1010), __byte_perm(s, s, 0x3232), o);
 #pragma unroll
       for (int c = 0; c < UC / 8; ++c) {
-        const int chunk = u * (UC / 8) + c;  // before the swap; D = 64: the half's own four chunks
-        const uint32_t at = TB ? static_cast<uint32_t>((chunk ^ x) << 4)
-                               : static_cast<uint32_t>(((chunk + half * 4) ^ (r & 7)) << 4);
-        sts128(row + at, make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]));
+        const uint32_t chunk = u * (UC / 8) + c;
+        sts128(row + (chunk / 8) * kTileBytes + (((chunk % 8) << 4) ^ x), make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]));
       }
     }
   }
@@ -204,10 +192,10 @@ struct Cfg {
 };
 
 struct Misc {
-  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full[2], drain;
+  uint64_t first[2], full[2], empty[2], s_full[2], p_full[2], o_full[2], begun, drain;
   uint32_t tmem;
   RowItem item;
-  uint32_t seen[kMasks][4];
+  alignas(16) uint32_t seen[kMasks][4];  // read 16 bytes at a time
   float mul[2][128];
 };
 static_assert(sizeof(Misc) <= 2048, "fits behind the rings");
@@ -259,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_tiles(const PagedArgs a) 
 
   // the merge kernel may start once every CTA has: its prologue reads inputs alone
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (warp == 16) find_item(a.cu_rows, a.S, a.n_rows, a.max_rows, SLOTS * a.T, idx, lane, &m->item);
+  if (warp == 12) find_item(a.cu_rows, a.S, a.n_rows, a.max_rows, SLOTS * a.T, idx, lane, &m->item);
   __syncthreads();
   const RowItem it = m->item;
   if (it.len == 0) return;
@@ -275,48 +263,60 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_tiles(const PagedArgs a) 
   if (k1 <= k0) return;  // no row of the tile sees a key here: the merge does not look
   const int n = (k1 - k0 + 127) >> 7;
 
-  if (warp == 16) tmem_alloc(&m->tmem, 512);
+  if (warp == 12) tmem_alloc(&m->tmem, 512);
   const int live_warps = min(4, (min(tokens, a.T) * a.g + 31) >> 5);  // of a slot, with rows of a token
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&m->k_full[i], kProdWarps), mbar_init(&m->v_full[i], kProdWarps);
-      mbar_init(&m->k_empty[i], 1), mbar_init(&m->v_empty[i], 1);
+      mbar_init(&m->first[i], kProdWarps), mbar_init(&m->full[i], kProdWarps), mbar_init(&m->empty[i], 1);
       mbar_init(&m->s_full[i], 1), mbar_init(&m->o_full[i], 1);
       mbar_init(&m->p_full[i], SHARED ? 4 : live_warps);
     }
-    mbar_init(&m->drain, 1);
+    mbar_init(&m->begun, 1), mbar_init(&m->drain, 1);
     fence_mbar_init();
   }
   // the query rows, rotated, scaled by a power of two into [1, 2) and rounded once to fp16
   {
-    constexpr int CH = D / 32;
-    for (int r = warp; r < tokens * a.g; r += kThreads / 32) {
-      const int tok = r / a.g, j = r - tok * a.g, t = tok / a.T, tr = r - t * a.T * a.g;
-      const __half* qp = a.q + (static_cast<int64_t>(it.row0) + it.q0 + tok) * a.q_stride + (h * a.g + j) * D;
-      float x[CH];
+    constexpr int CH = D / 32, AT = 4, WARPS = kThreads / 32;  // four rows of a warp on their way at a time
+    int ch[CH];
 #pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        const int ch = lane * CH + c;
-        x[c] = __half2float(qp[a.kperm ? a.kperm[h * D + ch] & (D - 1) : ch]);
+    for (int c = 0; c < CH; ++c) ch[c] = a.kperm ? a.kperm[h * D + lane * CH + c] & (D - 1) : lane * CH + c;
+    const int rows = tokens * a.g;
+    for (int r0 = warp; r0 < rows; r0 += AT * WARPS) {
+      __half raw[AT][CH];
+#pragma unroll
+      for (int k = 0; k < AT; ++k) {
+        const int r = min(r0 + k * WARPS, rows - 1), tok = r / a.g, j = r - tok * a.g;
+        const __half* qp = a.q + (static_cast<int64_t>(it.row0) + it.q0 + tok) * a.q_stride + (h * a.g + j) * D;
+#pragma unroll
+        for (int c = 0; c < CH; ++c) raw[k][c] = __ldg(qp + ch[c]);
       }
-      if (a.rot) {
-        warp_fwht<CH>(x, lane);
 #pragma unroll
-        for (int c = 0; c < CH; ++c) x[c] *= a.rscale;
+      for (int k = 0; k < AT; ++k) {
+        const int r = r0 + k * WARPS;
+        if (r >= rows) break;
+        const int tok = r / a.g, t = tok / a.T, tr = r - t * a.T * a.g;
+        float x[CH];
+#pragma unroll
+        for (int c = 0; c < CH; ++c) x[c] = __half2float(raw[k][c]);
+        if (a.rot) {
+          warp_fwht<CH>(x, lane);
+#pragma unroll
+          for (int c = 0; c < CH; ++c) x[c] *= a.rscale;
+        }
+        float top = 0.0f;
+#pragma unroll
+        for (int c = 0; c < CH; ++c) top = fmaxf(top, fabsf(x[c]));
+        top = all_max(top);
+        const int e = top > 0.0f && top < INFINITY ? static_cast<int>(__float_as_uint(top) >> 23) - 127 : 0;
+        const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+          const int p = tile_pos<BITS>(lane * CH + c);
+          *reinterpret_cast<__half*>(gbase + t * C::kHead + (p / 64) * kTileBytes + sw128(tr, (p % 64) / 8) + 2 * (p % 8)) =
+              __float2half_rn(x[c] * down);
+        }
+        if (lane == 0) m->mul[t][tr] = a.scale * 1.4426950408889634f * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
       }
-      float top = 0.0f;
-#pragma unroll
-      for (int c = 0; c < CH; ++c) top = fmaxf(top, fabsf(x[c]));
-      top = all_max(top);
-      const int e = top > 0.0f && top < INFINITY ? static_cast<int>(__float_as_uint(top) >> 23) - 127 : 0;
-      const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-#pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        const int p = tile_pos<BITS>(lane * CH + c);
-        *reinterpret_cast<__half*>(gbase + t * C::kHead + (p / 64) * kTileBytes + sw128(tr, (p % 64) / 8) + 2 * (p % 8)) =
-            __float2half_rn(x[c] * down);
-      }
-      if (lane == 0) m->mul[t][tr] = a.scale * 1.4426950408889634f * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
     }
     fence_async_smem();
   }
@@ -324,20 +324,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_tiles(const PagedArgs a) 
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = m->tmem;
-  // tiles of keys of each slot
+  // tiles of keys of each slot: all, or every other one
   int n_t[2];
-  if (SHARED) {
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const int last = min(k1, pos0 + min(tokens, (t + 1) * a.T));
-      n_t[t] = tokens > t * a.T && last > k0 ? (last - k0 + 127) >> 7 : 0;
-    }
-  } else {
-    n_t[0] = (n + 1) >> 1;
-    n_t[1] = n >> 1;
+  for (int t = 0; t < 2; ++t) {
+    const int last = min(k1, pos0 + min(tokens, (t + 1) * a.T));
+    n_t[t] = !SHARED ? (n + 1 - t) >> 1 : tokens > t * a.T && last > k0 ? (last - k0 + 127) >> 7 : 0;
   }
 
   if (warp < 8) {
+    more_regs<kRegsSoftmax>();
     const int t = warp >> 2, tq = SHARED ? t : 0;
     const int r = tid & 127, tok = tq * a.T + r / a.g, j = r % a.g;
     const bool mine = r < a.T * a.g && tok < tokens;
@@ -346,28 +342,28 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_tiles(const PagedArgs a) 
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(warp & 3) << 21);
     const uint32_t s_addr = lane_base + 128 * t, o_addr = lane_base + 256 + D * t;
     RowStat st;
+    if (!mine) st.m = 0.0f;  // whatever a row of no token holds, it asks for no rescaling below
     bool ok = true;
     const bool works = SHARED || (warp & 3) < live_warps;
     const int nt = works ? n_t[t] : 0;
     for (int i = 0; i < nt; ++i) {
-      ok = __all_sync(0xffffffffu, mbar_wait(&m->s_full[t], i & 1, a.wait_ns, a.err));
+      ok = warp_wait(&m->s_full[t], i & 1, a.wait_ns, a.err);
       if (!ok) break;
       tc_fence_after();
       const int tile = SHARED ? i : 2 * i + t;
       const uint4 bits = *reinterpret_cast<const uint4*>(m->seen[tile % kMasks]);
       const int left = lim - (k0 + 128 * tile);
-      const bool whole = left >= 128 && (bits.x & bits.y & bits.z & bits.w) == 0xffffffffu;
       const uint32_t seen[4] = {bits.x & first_bits(left, 0), bits.y & first_bits(left, 32),
                                 bits.z & first_bits(left, 64), bits.w & first_bits(left, 96)};
-      if (__all_sync(0xffffffffu, whole))
-        softmax_tile<__half, D, false, false>(s_addr, o_addr, i > 0, mul, st, seen);
+      if (__all_sync(0xffffffffu, (seen[0] & seen[1] & seen[2] & seen[3]) == 0xffffffffu))
+        softmax_tile<__half, D, false, true>(s_addr, o_addr, i > 0, mul, st, seen);
       else
-        softmax_tile<__half, D, true, false>(s_addr, o_addr, i > 0, mul, st, seen);
+        softmax_tile<__half, D, true, true>(s_addr, o_addr, i > 0, mul, st, seen);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&m->p_full[t]);
     }
-    if (ok && nt > 0) ok = __all_sync(0xffffffffu, mbar_wait(&m->o_full[t], 0, a.wait_ns, a.err));
+    if (ok && nt > 0) ok = warp_wait(&m->o_full[t], 0, a.wait_ns, a.err);
     if (ok && works) {
       const size_t at = static_cast<size_t>(SHARED ? z : 2 * z + t) * (static_cast<size_t>(a.n_rows) * a.Hq) +
                         (static_cast<size_t>(it.row0) + it.q0 + tok) * a.Hq + h * a.g + j;
@@ -387,204 +383,268 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_tiles(const PagedArgs a) 
         }
       }
     }
-  } else if (warp < 16) {
-    const int p = tid - 256, r = p >> 1, half = p & 1;
-    using R = Half<D, BITS, G>;
+  } else if (warp < 12) {
+    fewer_regs<kRegsRecords>();
+    const int r = tid - 256;  // this thread's key of each tile
+    using R = Record<D, BITS, G>;
     const int32_t* table = a.block_table + static_cast<size_t>(it.seq) * a.max_pages;
-    // page of this thread's key of tile i; -1 outside the stretch, among the sinks, behind the last tile
-    auto page_of = [&](int i) {
-      if (i >= n) return -1;
-      const int pos = k0 + 128 * i + r;
-      if (pos >= k1 || pos < a.n_sink) return -1;
-      const int pg = __ldg(table + a.div_ps.div(static_cast<uint32_t>(pos)));
-      return pg < a.n_pages ? pg : -1;
+    // record of the key of tile i; live is false outside the stretch, among the sinks, without a page
+    struct Place {
+      size_t rec;
+      bool live;
     };
-    auto fetch = [&](int i, int pg, R& k, R& v) {
-      if (pg < 0) {
-        k.clear();
-        v.clear();
-        return;
-      }
-      const uint32_t pos = static_cast<uint32_t>(k0 + 128 * i + r);
-      const size_t rec = (static_cast<size_t>(pg) * a.H + h) * a.div_ps.d + a.div_ps.mod(pos, a.div_ps.div(pos));
-      k.load(a.kcodes, a.ksz, rec, half);
-      v.load(a.vcodes, a.vsz, rec, half);
+    auto look_up = [&](int i) {
+      Place p{0, false};
+      if (i >= n) return p;
+      const int pos = k0 + 128 * i + r;
+      if (pos >= k1 || pos < a.n_sink) return p;
+      const uint32_t e = a.div_ps.div(static_cast<uint32_t>(pos));
+      const int pg = __ldg(table + e);
+      p.live = pg >= 0 && pg < a.n_pages;
+      if (p.live) p.rec = (static_cast<size_t>(pg) * a.H + h) * a.div_ps.d + a.div_ps.mod(static_cast<uint32_t>(pos), e);
+      return p;
     };
     bool ok = true;
-    auto put = [&](int i, const R& x, uint64_t* full, uint64_t* empty, uint32_t ring) {
-      const int s = i & 1;
-      if (i >= 2) ok = ok && mbar_wait(&empty[s], ((i >> 1) & 1) ^ 1, a.wait_ns, a.err);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) return;
-      x.store(base + ring + s * C::kHead, r, half);
+    const uint32_t ks = base + C::kK, vs = base + C::kV;  // two stages of each, by the tile's parity
+    auto done = [&](uint64_t* bar) {
       fence_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&full[s]);
+      if (lane == 0) mbar_arrive(bar);
     };
-    // records two tiles ahead in registers, their pages three; K_i goes in before V_(i + 1 - kAhead)
-    R kr[2], vr[2], vlate;
-    int pg[2] = {page_of(0), page_of(1)}, pn = page_of(2);
-    fetch(0, pg[0], kr[0], vr[0]);
-    fetch(1, pg[1], kr[1], vr[1]);
-    for (int i0 = 0; ok && i0 < n + C::kAhead - 1; i0 += 2) {
+    auto note = [&](int i, const Place& p) {  // the keys that are there
+      const uint32_t seen = __ballot_sync(0xffffffffu, p.live);
+      if (lane == 0) m->seen[i % kMasks][warp - 8] = seen;
+    };
+    // K_0 .. K_(A-1) alone, then pairs (V_j, K_(j+A)); a record is asked for as soon as its registers are free
+    constexpr int A = C::kAhead;
+    R kr, vr;
+    Place kp = look_up(0), vp = kp, kn = look_up(1);
+    kr.load(a.kcodes, a.ksz, kp.rec, kp.live);
+    vr.load(a.vcodes, a.vsz, vp.rec, vp.live);
+    Place v2 = kn;  // the tile behind V's
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const int i = i0 + b;
-        if (i < n) {
-          const uint32_t seen = __ballot_sync(0xffffffffu, pg[b] >= 0);
-          if (lane == 0) {  // two lanes a key
-            uint32_t x = seen & 0x55555555u;
-            x = (x | (x >> 1)) & 0x33333333u;
-            x = (x | (x >> 2)) & 0x0f0f0f0fu;
-            x = (x | (x >> 4)) & 0x00ff00ffu;
-            x = (x | (x >> 8)) & 0x0000ffffu;
-            reinterpret_cast<uint16_t*>(m->seen[i % kMasks])[warp - 8] = static_cast<uint16_t>(x);
-          }
-          put(i, kr[b], m->k_full, m->k_empty, C::kK);
-        }
-        const int j = i + 1 - C::kAhead;
-        if (j >= 0 && j < n) put(j, C::kAhead == 1 ? vr[b] : vlate, m->v_full, m->v_empty, C::kV);
-        if (!ok) break;
-        if (C::kAhead == 2) vlate = vr[b];
-        pg[b] = pn;
-        fetch(i + 2, pg[b], kr[b], vr[b]);
-        pn = page_of(i + 3);
+    for (int i = 0; i < A; ++i) {
+      if (i < n) {
+        note(i, kp);
+        kr.store(ks + (i & 1) * C::kHead, r);
+        done(&m->first[i]);
       }
+      kp = kn;
+      kr.load(a.kcodes, a.ksz, kp.rec, kp.live);
+      kn = look_up(i + 2);
+    }
+    for (int j = 0; j < n; ++j) {
+      const int s = j & 1;
+      if (j >= 2) ok = warp_wait(&m->empty[s], ((j >> 1) & 1) ^ 1, a.wait_ns, a.err);
+      if (ok && j == 2 - A) ok = warp_wait(&m->begun, 0, a.wait_ns, a.err);  // K_2 takes the place of K_0
+      if (!ok) break;
+      vr.store(vs + s * C::kHead, r);
+      vp = v2;
+      v2 = A == 1 ? kn : kp;
+      vr.load(a.vcodes, a.vsz, vp.rec, vp.live);
+      if (j + A < n) {
+        note(j + A, kp);
+        kr.store(ks + ((j + A) & 1) * C::kHead, r);
+        kp = kn;
+        kr.load(a.kcodes, a.ksz, kp.rec, kp.live);
+        kn = look_up(j + A + 2);
+      }
+      done(&m->full[s]);
     }
   } else {
-    if (lane == 0) {
+    fewer_regs<kRegsIssue>();
+    if (warp == 12) {
       bool ok = true;
-      auto wait = [&](uint64_t* bar, uint32_t parity) {
-        ok = ok && mbar_wait(bar, parity, a.wait_ns, a.err);
-        return ok;
-      };
+      auto wait = [&](uint64_t* bar, uint32_t parity) { ok = ok && warp_wait(bar, parity, a.wait_ns, a.err); };
       auto scores = [&](int t, int j) {
         issue_scores<__half, D>(tmem + 128 * t, base + (SHARED ? t : 0) * C::kHead, base + C::kK + (j & 1) * C::kHead);
         tc_commit(&m->s_full[t]);
       };
-      auto values = [&](int t, int j, bool acc) {
-        issue_values<__half, D>(tmem + 256 + D * t, tmem + 128 * t, base + C::kV + (j & 1) * C::kHead, acc);
+      // the weights of slot t for tile j, then the scores that replace them (products run in order)
+      auto turn = [&](int t, int i, int j, int next) {
+        wait(&m->p_full[t], i & 1);
+        if (!ok) return;
+        tc_fence_after();
+        issue_values<__half, D>(tmem + 256 + D * t, tmem + 128 * t, base + C::kV + (j & 1) * C::kHead, i > 0);
+        if (i + 1 < n_t[t]) scores(t, next);
+        else tc_commit(&m->o_full[t]);
       };
       if (SHARED) {
-        if (wait(&m->k_full[0], 0)) {
-          for (int t = 0; t < 2; ++t)
-            if (n_t[t] > 0) scores(t, 0);
-          tc_commit(&m->k_empty[0]);
-        }
-        for (int j = 0; ok && j < n; ++j) {
-          wait(&m->v_full[j & 1], (j >> 1) & 1);
-          if (j + 1 < n) wait(&m->k_full[(j + 1) & 1], ((j + 1) >> 1) & 1);
-          for (int t = 0; ok && t < 2; ++t) {
-            if (j >= n_t[t] || !wait(&m->p_full[t], j & 1)) continue;
-            tc_fence_after();
-            values(t, j, j > 0);
-            if (j + 1 < n_t[t]) scores(t, j + 1);
-            else tc_commit(&m->o_full[t]);
-          }
-          if (!ok) break;
-          tc_commit(&m->v_empty[j & 1]);
-          if (j + 1 < n) tc_commit(&m->k_empty[(j + 1) & 1]);
-        }
+        wait(&m->first[0], 0);
+        for (int t = 0; ok && t < 2; ++t)
+          if (n_t[t] > 0) scores(t, 0);
       } else {
-        for (int j = 0; j < 2 && j < n; ++j)
-          if (wait(&m->k_full[j], 0)) {
-            scores(j, j);
-            tc_commit(&m->k_empty[j]);
-          }
-        for (int j = 0; ok && j < n; ++j) {
-          const int t = j & 1;
-          wait(&m->v_full[t], (j >> 1) & 1);
-          if (j + 2 < n) wait(&m->k_full[t], ((j + 2) >> 1) & 1);
-          if (!wait(&m->p_full[t], (j >> 1) & 1)) break;
-          tc_fence_after();
-          values(t, j, j > 1);
-          tc_commit(&m->v_empty[t]);
-          if (j + 2 < n) {
-            scores(t, j + 2);
-            tc_commit(&m->k_empty[t]);
-          } else {
-            tc_commit(&m->o_full[t]);
-          }
+        for (int j = 0; j < 2 && j < n; ++j) {
+          wait(&m->first[j], 0);
+          if (ok) scores(j, j);
         }
+      }
+      if (ok) tc_commit(&m->begun);
+      for (int j = 0; ok && j < n; ++j) {
+        wait(&m->full[j & 1], (j >> 1) & 1);
+        if (SHARED) {
+          for (int t = 0; ok && t < 2; ++t)
+            if (j < n_t[t]) turn(t, j, j, j + 1);
+        } else if (ok) {
+          turn(j & 1, j >> 1, j, j + 2);
+        }
+        if (ok) tc_commit(&m->empty[j & 1]);
       }
       if (!ok) {  // a wait ran out: the products in flight still end before the memory is given back
         tc_commit(&m->drain);
-        mbar_wait(&m->drain, 0, a.wait_ns, a.err);
+        warp_wait(&m->drain, 0, a.wait_ns, a.err);
       }
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 16) tmem_dealloc(tmem, 512);
+  if (warp == 12) tmem_dealloc(tmem, 512);
 }
 
-// One warp per row and query head, C = D / 32 channels a lane.
-template <int D, int BITS>
+// C fp16 values as fp32, one load.
+template <int C>
+__device__ __forceinline__ void ld_halves(const __half* p, float (&x)[C]) {
+  static_assert(C == 2 || C == 4, "D / 32");
+  uint32_t w[C / 2];
+  if constexpr (C == 4) {
+    const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+    w[0] = v.x, w[1] = v.y;
+  } else {
+    w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+  }
+#pragma unroll
+  for (int i = 0; i < C / 2; ++i) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+    x[2 * i] = f.x, x[2 * i + 1] = f.y;
+  }
+}
+
+// Sink row n of K turned to its position: this lane's C channels, in the fma order of rope_fwd.
+template <int D, int C>
+__device__ __forceinline__ void sink_key(const PagedArgs& a, const __half* row, int n, int lane, float (&x)[C]) {
+  ld_halves<C>(row + lane * C, x);
+  if (a.rope == 0) return;
+  const float2* cs = reinterpret_cast<const float2*>(a.rope_cs) + static_cast<size_t>(n) * (D / 2);
+  if (a.rope == 1) {
+#pragma unroll
+    for (int c = 0; c < C; c += 2) {
+      const float2 t = __ldg(cs + (lane * C + c) / 2);
+      rope_fwd(x[c], x[c + 1], t.x, t.y);
+    }
+  } else {
+    const bool up = lane >= 16;  // channels of the upper half
+    float y[C];
+    ld_halves<C>(row + (lane ^ 16) * C, y);
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const float2 t = __ldg(cs + (lane & 15) * C + c);
+      float lo = up ? y[c] : x[c], hi = up ? x[c] : y[c];
+      rope_fwd(lo, hi, t.x, t.y);
+      x[c] = up ? hi : lo;
+    }
+  }
+}
+
+// The last sequence whose first row is at or before `row`: 32 offsets at a time. One warp.
+__device__ __forceinline__ int seq_of_row(const int32_t* cu_rows, int S, int row, int lane) {
+  int lo = 0, hi = S;
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) >> 5, at = lo + lane * step;
+    const uint32_t before = __ballot_sync(0xffffffffu, at < hi && __ldg(cu_rows + at) <= row);
+    lo += before ? (31 - __clz(before)) * step : 0;
+    if (!before) break;
+    hi = min(hi, lo + step);
+  }
+  return lo;
+}
+
+// W warps per row and query head (a CTA has 8), C = D / 32 channels a lane. TILE: the parts' channels
+// are in tile order. The parts of a row are joined in a fixed order: warp w takes parts w, w + W, ...,
+// and warp 0 the sinks before them. A row is a chain of dependent loads (its sequence, lengths, sinks,
+// statistics, sums), which is what this kernel's time is; each link is read for four sinks or parts at
+// a time.
+template <int D, int BITS, bool TILE, int W>
 __global__ void __launch_bounds__(256) k_paged_merge(const PagedArgs a) {
   constexpr int C = D / 32;
   __shared__ float nat[8][D];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const long long wi = blockIdx.x * 8ll + warp;
+  __shared__ float wtop[8], wsum[8];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, w = warp % W;
+  const long long wi = (blockIdx.x * 8ll + warp) / W;
   const int row = static_cast<int>(wi / a.Hq), qh = static_cast<int>(wi % a.Hq);
-  if (row >= a.n_rows) return;
-  // the sequence whose rows hold this one
-  int lo = 0, hi = a.S;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (__ldg(a.cu_rows + mid) <= row) lo = mid; else hi = mid;
-  }
+  if (row >= a.n_rows) return;  // the W warps of a row agree, here and below
+  const int lo = seq_of_row(a.cu_rows, a.S, row, lane);
   const int b = min(max(__ldg(a.cu_rows + lo), 0), a.n_rows), e = min(max(__ldg(a.cu_rows + lo + 1), b), a.n_rows);
-  if (row < b || row >= e || row - b >= a.max_rows) return;
   const int h = qh / a.g, len = max(__ldg(a.kv_len + lo), 0);
+  if (row < b || row >= e || row - b >= a.max_rows) return;
   // keys [0, lim)
   const int lim = min(len - (e - b) + (row - b) + 1, min(len, sat_pages(a.max_pages, static_cast<int>(a.div_ps.d))));
   const float unit = a.scale * 1.4426950408889634f;
   float top = -INFINITY, total = 0.0f, own[C];
 #pragma unroll
   for (int c = 0; c < C; ++c) own[c] = 0.0f;
-  if (a.n_sink > 0) {  // the sinks' running sums, in their own basis
+  if (a.n_sink > 0 && w == 0) {  // the sinks' running sums, in their own basis
+    constexpr int B = 4;
     const int srow = a.sink_slot ? __ldg(a.sink_slot + lo) : lo;
-    const __half* qp = a.q + row * a.q_stride + qh * D + lane * C;
-    float q[C];
-#pragma unroll
-    for (int c = 0; c < C; ++c) q[c] = __half2float(qp[c]);
     const int last = srow >= 0 && srow < a.sink_rows ? min(a.n_sink, lim) : 0;
-    for (int n = 0; n < last; ++n) {
-      const int pg = __ldg(a.block_table + static_cast<size_t>(lo) * a.max_pages + a.div_ps.div(static_cast<uint32_t>(n)));
-      if (pg < 0 || pg >= a.n_pages || (a.rope && n >= a.rope_rows)) continue;
-      const size_t at = ((static_cast<size_t>(srow) * a.H + h) * a.n_sink + n) * D;
-      float s = 0.0f;
+    const size_t first = (static_cast<size_t>(max(srow, 0)) * a.H + h) * a.n_sink * D;
+    float q[C];
+    ld_halves<C>(a.q + row * a.q_stride + qh * D + lane * C, q);
+    for (int n0 = 0; n0 < last; n0 += B) {
+      float s[B], v[B][C];
 #pragma unroll
-      for (int c = 0; c < C; ++c) {
-        const int j = lane * C + c;
-        float x = __half2float(a.ksink[at + j]);
-        if (a.rope) {
-          const bool pairs = a.rope == 1;
-          const int j2 = pairs ? j ^ 1 : (j + D / 2) % D, pr = pairs ? j / 2 : j % (D / 2);
-          const float2 cs = reinterpret_cast<const float2*>(a.rope_cs)[static_cast<size_t>(n) * (D / 2) + pr];
-          const float x2 = __half2float(a.ksink[at + j2]);
-          x = (pairs ? (j & 1) != 0 : j >= D / 2) ? fmaf(x2, cs.y, x * cs.x) : fmaf(x, cs.x, -(x2 * cs.y));
+      for (int i = 0; i < B; ++i) {
+        const int n = n0 + i;
+        s[i] = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < C; ++c) v[i][c] = 0.0f;
+        if (n >= last || (a.rope && n >= a.rope_rows)) continue;
+        const int pg = __ldg(a.block_table + static_cast<size_t>(lo) * a.max_pages + a.div_ps.div(static_cast<uint32_t>(n)));
+        float k[C];
+        sink_key<D, C>(a, a.ksink + first + static_cast<size_t>(n) * D, n, lane, k);
+        ld_halves<C>(a.vsink + first + static_cast<size_t>(n) * D + lane * C, v[i]);
+        float dot = 0.0f;
+#pragma unroll
+        for (int c = 0; c < C; ++c) dot = fmaf(q[c], k[c], dot);
+        dot = all_sum(dot) * unit;
+        if (pg >= 0 && pg < a.n_pages) {
+          s[i] = dot;
+        } else {
+#pragma unroll
+          for (int c = 0; c < C; ++c) v[i][c] = 0.0f;
         }
-        s = fmaf(q[c], x, s);
       }
-      s = all_sum(s) * unit;
-      const float mn = fmaxf(top, s), f = top == mn ? 1.0f : exp2f(top - mn), p = exp2f(s - mn);
+      const float mn = fmaxf(fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3])), top), ref = mn == -INFINITY ? 0.0f : mn;
+      const float f = exp2f(top - ref);
       top = mn;
-      total = fmaf(total, f, p);
+      total *= f;
 #pragma unroll
-      for (int c = 0; c < C; ++c) own[c] = own[c] * f + p * __half2float(a.vsink[at + lane * C + c]);
+      for (int c = 0; c < C; ++c) own[c] *= f;
+#pragma unroll
+      for (int i = 0; i < B; ++i) {
+        const float p = exp2f(s[i] - ref);
+        total += p;
+#pragma unroll
+        for (int c = 0; c < C; ++c) own[c] = fmaf(p, v[i][c], own[c]);
+      }
     }
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  // the stretches that hold keys of this row, an empty one (weight total 0) left out
+  // the stretches that hold keys of this row, an empty part (weight total 0) left out
   const size_t rows = static_cast<size_t>(a.n_rows) * a.Hq, me = static_cast<size_t>(row) * a.Hq + qh;
   const int per = a.n_parts / a.n_stretch;
   const int parts = lim > 0 ? min(a.n_stretch, (lim - 1) / a.stretch + 1) * per : 0;
+  auto part = [&](int p) { return p < parts ? a.part_s[p * rows + me] : make_float2(-INFINITY, 0.0f); };
   float all_top = top;
-  for (int p0 = 0; p0 < parts; p0 += 32) {
-    const float2 s = p0 + lane < parts ? a.part_s[(p0 + lane) * rows + me] : make_float2(-INFINITY, 0.0f);
+  for (int p0 = w; p0 < parts; p0 += 32 * W) {
+    const float2 s = part(p0 + lane * W);
     all_top = fmaxf(all_top, all_max(s.y != 0.0f ? s.x : -INFINITY));
+  }
+  if constexpr (W > 1) {
+    if (lane == 0) wtop[warp] = all_top;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < W; ++i) all_top = fmaxf(all_top, wtop[i]);
   }
   const float ref = all_top == -INFINITY ? 0.0f : all_top;
   float o[C];
@@ -592,14 +652,46 @@ __global__ void __launch_bounds__(256) k_paged_merge(const PagedArgs a) {
 #pragma unroll
   for (int c = 0; c < C; ++c) o[c] = 0.0f, own[c] *= fs;
   total *= fs;
-  for (int p = 0; p < parts; ++p) {
-    const float2 s = a.part_s[p * rows + me];
-    if (s.y == 0.0f) continue;
-    const float f = exp2f(s.x - ref);
-    total = fmaf(s.y, f, total);
-    const float* src = a.part_o + (p * rows + me) * D;
+  for (int p0 = w; p0 < parts; p0 += 32 * W) {
+    const float2 s = part(p0 + lane * W);
+    const bool live = s.y != 0.0f;
+    const float f = live ? exp2f(s.x - ref) : 0.0f;
+    total += all_sum(live ? s.y * f : 0.0f);
+    const uint32_t has = __ballot_sync(0xffffffffu, live);
+    const int n = min(32, (parts - p0 + W - 1) / W);
+    for (int i0 = 0; i0 < n; i0 += 4) {
+      float x[4][C];
 #pragma unroll
-    for (int c = 0; c < C; ++c) o[c] = fmaf(src[tile_pos<BITS>(lane * C + c)], f, o[c]);
+      for (int i = 0; i < 4; ++i) {
+#pragma unroll
+        for (int c = 0; c < C; ++c) x[i][c] = 0.0f;
+        if (i0 + i < 32 && (has >> (i0 + i)) & 1u) {  // what an empty part's sums hold is not read
+          const float* src = a.part_o + (static_cast<size_t>(p0 + (i0 + i) * W) * rows + me) * D;
+#pragma unroll
+          for (int c = 0; c < C; ++c) x[i][c] = src[TILE ? tile_pos<BITS>(lane * C + c) : lane * C + c];
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float fi = __shfl_sync(0xffffffffu, f, (i0 + i) & 31);
+#pragma unroll
+        for (int c = 0; c < C; ++c) o[c] = fmaf(x[i][c], i0 + i < n ? fi : 0.0f, o[c]);
+      }
+    }
+  }
+  if constexpr (W > 1) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) nat[warp][lane * C + c] = o[c];
+    if (lane == 0) wsum[warp] = total;
+    __syncthreads();
+    if (w > 0) return;
+#pragma unroll
+    for (int i = 1; i < W; ++i) {
+      total += wsum[i];
+#pragma unroll
+      for (int c = 0; c < C; ++c) o[c] += nat[i][lane * C + c];
+    }
+    __syncwarp();
   }
   if (a.rot) {
     warp_fwht<C>(o, lane);
@@ -637,10 +729,10 @@ __global__ void __launch_bounds__(256) k_paged_merge(const PagedArgs a) {
 //           (A = 16 channels x 16 keys of codes, B = weights)
 // A weight p S is at most 2^15: the reference m follows s + log2 S (S >= 2^-30)
 // and is raised when that exceeds it by 2^8; p = 2^(s - m + 7).
-constexpr int kFewWarps = 8;
+constexpr int kFewWarps = 4;
 constexpr int kFewThreads = 32 * kFewWarps;
 constexpr int kBlock = 16;
-static_assert(kFewWarps * kBlock == 128, "a warp's next block is 128 keys on");
+constexpr int kFewStep = kFewWarps * kBlock;  // keys between a warp's blocks
 constexpr float kFewUp = 7.0f;
 constexpr float kFewMinS = 9.3132257e-10f;  // 2^-30
 
@@ -665,6 +757,10 @@ struct Map<2, G> {
   static constexpr int kDown = 10;  // pairs 5 .. 7 are read after this shift
   static __host__ __device__ constexpr bool shifted(int p) { return p >= 5; }
   static __host__ __device__ constexpr int bit(int p) { return 2 * (p >= 5 ? p - 5 : p); }
+  // a value's code c: from the register shifted by vshift (left if positive), at bit vbit
+  static __device__ __forceinline__ uint32_t vshift(uint32_t y, int k) { return k == 0 ? y << 4 : k == 1 ? y : y >> 6; }
+  static __host__ __device__ constexpr int vset(int c) { return c < 2 ? 0 : c < 5 ? 1 : 2; }
+  static __host__ __device__ constexpr int vbit(int c) { return c < 2 ? 4 + 2 * c : c < 5 ? 2 * c : 2 * c - 6; }
   static __host__ __device__ constexpr int group(int i) { return kFine ? i : i * 64 / G; }
   // values
   static constexpr int kVWords = G == 128 ? 1 : G == 64 ? 2 : 4;
@@ -700,6 +796,9 @@ struct Map<4, G> {
   static __device__ __forceinline__ int kch(int i, int p, int tig) { return 8 * kword(i, tig) + p; }
   static __host__ __device__ constexpr bool shifted(int p) { return p >= 2; }
   static __host__ __device__ constexpr int bit(int p) { return 4 * (p & 1); }
+  static __device__ __forceinline__ uint32_t vshift(uint32_t y, int k) { return k == 0 ? y << 4 : k == 1 ? y : y >> (4 * k - 4); }
+  static __host__ __device__ constexpr int vset(int c) { return c; }
+  static __host__ __device__ constexpr int vbit(int) { return 4; }
   static __host__ __device__ constexpr int group(int i) { return 32 * i / G; }
   static constexpr int kVWords = kFine ? 4 : 2, kVRegs = 4;
   static __device__ __forceinline__ int vword(int i, int gr) { return kFine ? 4 * i + (gr & 3) : gr + 8 * i; }
@@ -743,14 +842,13 @@ __device__ __forceinline__ float2 h2f2(uint32_t w) { return __half22float2(*rein
 
 // NT: column tiles, 4 rows each. One CTA per (stretch of keys, KV head, sequence).
 template <int BITS, int G, int NT>
-__global__ void __launch_bounds__(kFewThreads, NT == 1 ? 2 : 1) k_paged_few(const PagedArgs a) {
+__global__ void __launch_bounds__(kFewThreads, NT == 1 ? 4 : 2) k_paged_few(const PagedArgs a) {
   using C = FewCfg<BITS, G>;
   using M = Map<BITS, G>;
   constexpr int D = 128, NG = C::kNG, RB = C::kRec, ST = C::kStages, R = 4 * NT;
   extern __shared__ __align__(128) uint8_t few_smem[];
   __shared__ float qrow[R][D];
   __shared__ float qmul[R], qsum[R][NG];
-  __shared__ float wm[kFewWarps][R], wl[kFewWarps][R];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int gr = lane >> 2, tig = lane & 3;
   unsigned rest = blockIdx.x;
@@ -793,7 +891,7 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 2 : 1) k_paged_few(cons
       const int pg = __ldg(table + entry);
       k.page = pg < a.n_pages ? pg : -1;
     }
-    pos = min(pos, k1) + kFewWarps * kBlock;
+    pos = min(pos, k1) + kFewStep;
     entry += a.step_page;
     off += a.step_off;
     if (off >= ps) off -= ps, ++entry;
@@ -865,14 +963,14 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 2 : 1) k_paged_few(cons
     if (lane == 0) qmul[r] = unit * __uint_as_float(static_cast<uint32_t>(127 - 13 + e) << 23) * 16777216.0f;
   }
   __syncthreads();
-  // B fragments of the scores: column gr of tile t is row 4 t + gr / 2, term gr & 1. Each warp makes one k-step.
+  // B fragments of the scores: column gr of tile t is row 4 t + gr / 2, term gr & 1. Each warp makes two k-steps.
   __shared__ uint2 frag[NT][8][32];
   {
     constexpr int PK = M::kPairs / 2;  // k-steps of a word
     uint32_t b2[NT][2];
 #pragma unroll
     for (int ks = 0; ks < 8; ++ks) {
-      if (ks != warp) continue;
+      if (ks % kFewWarps != warp) continue;
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         const float* q = qrow[4 * t + (gr >> 1)];
@@ -925,7 +1023,7 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 2 : 1) k_paged_few(cons
 
   uint32_t stage = 0;
   int n0 = k0 + warp * kBlock;
-  for (int i = 0; i < mine; ++i, n0 += kFewWarps * kBlock) {
+  for (int i = 0; i < mine; ++i, n0 += kFewStep) {
     cp_async_wait_group<ST - 1>();
     __syncwarp();
     const uint8_t* st = wgen + stage;
@@ -1031,7 +1129,7 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 2 : 1) k_paged_few(cons
     // ---- values
     {
       const uint8_t* v0 = st + kBlock * RB + 2 * tig * RB;
-      uint32_t y[2][M::kVRegs], yd[2][M::kVRegs];
+      uint32_t y[2][M::kVRegs];
 #pragma unroll
       for (int w = 0; w < M::kVWords; ++w) {
         const int at = 4 * M::vword(w, gr);
@@ -1042,8 +1140,6 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 2 : 1) k_paged_few(cons
           if (M::vwordof(r) == w) {
             y[0][r] = M::vopen(r, u0, u1, gr);
             y[1][r] = M::vopen(r, u8, u9, gr);
-            yd[0][r] = y[0][r] >> M::kDown;
-            yd[1][r] = y[1][r] >> M::kDown;
           }
       }
 #pragma unroll
@@ -1055,7 +1151,7 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 2 : 1) k_paged_few(cons
 #pragma unroll
           for (int b = 0; b < 2; ++b) {
             const int c = M::vcode(mt, r8), r = M::vreg(mt, r8);
-            x[r8][b] = (M::shifted(c) ? yd[b][r] : y[b][r]) & ((F | F << 16) << M::bit(c));
+            x[r8][b] = M::vshift(y[b][r], M::vset(c)) & ((F | F << 16) << M::vbit(c));
           }
 #pragma unroll
         for (int t = 0; t < NT; ++t)
@@ -1070,7 +1166,8 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 2 : 1) k_paged_few(cons
   }
   cp_async_wait_all();
 
-  // ---- the warps' sums, joined in a fixed order
+  // ---- every warp leaves a part of its own, channels in their natural order
+  const size_t part = static_cast<size_t>(z * kFewWarps + warp) * (static_cast<size_t>(a.n_rows) * a.Hq);
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
 #pragma unroll
@@ -1079,48 +1176,34 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 2 : 1) k_paged_few(cons
 #pragma unroll
       for (int k = 0; k < NG; ++k) zr[t][k] += __shfl_xor_sync(0xffffffffu, zr[t][k], o);
     }
-    if (gr == 0) {
-      wm[warp][4 * t + tig] = mr[t];
-      wl[warp][4 * t + tig] = lr[t];
-    }
-  }
-  __syncthreads();  // every warp has left its ring: it holds the sums now
-  float* sums = reinterpret_cast<float*>(few_smem);  // [warp][row][channel]
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
     const int r = 4 * t + tig;
-    float top = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < kFewWarps; ++w) top = fmaxf(top, wm[w][r]);
-    const float f = mr[t] == -INFINITY ? 0.0f : exp2_fast(mr[t] - top);
+    if (r >= n_rows) continue;
+    const size_t at = part + (static_cast<size_t>(row0) + r / a.g) * a.Hq + h * a.g + r % a.g;
+    if (gr == 0) a.part_s[at] = make_float2(mr[t] - kFewUp, lr[t]);
+    if (lr[t] == 0.0f) continue;  // the merge does not read on
 #pragma unroll
     for (int mt = 0; mt < 8; ++mt)
 #pragma unroll
-      for (int r8 = 0; r8 < 2; ++r8) {
-        const float up = 16777216.0f / static_cast<float>(1 << M::bit(M::vcode(mt, r8)));
-        // the zeros' part is the same for the channels of a group
-        sums[(warp * R + r) * D + M::vch(mt, r8, gr)] =
-            fmaf(acc[mt][t][2 * r8] + acc[mt][t][2 * r8 + 1], up, zr[t][M::vgroup(mt)]) * f;
+      for (int r8 = 0; r8 < 2; ++r8) {  // the zeros' part is the same for the channels of a group
+        const float up = 16777216.0f / static_cast<float>(1 << M::vbit(M::vcode(mt, r8)));
+        acc[mt][t][2 * r8] = fmaf(acc[mt][t][2 * r8] + acc[mt][t][2 * r8 + 1], up, zr[t][M::vgroup(mt)]);
       }
-  }
-  __syncthreads();
-  const size_t part = static_cast<size_t>(z) * (static_cast<size_t>(a.n_rows) * a.Hq);
-  for (int e = tid; e < n_rows * D; e += kFewThreads) {
-    const int r = e / D, ch = e % D;
-    float o = 0.0f;
+    float* dst = a.part_o + at * D;
+    constexpr int RUN = G == 128 && BITS == 2 ? 8 : G == 32 ? 2 : 4;  // neighbouring channels in neighbouring m-tiles
 #pragma unroll
-    for (int w = 0; w < kFewWarps; ++w) o += sums[(w * R + r) * D + ch];
-    const size_t at = part + (static_cast<size_t>(row0) + r / a.g) * a.Hq + h * a.g + r % a.g;
-    a.part_o[at * D + tile_pos<BITS>(ch)] = o;
-  }
-  if (tid < n_rows) {
-    float top = -INFINITY, l = 0.0f;
+    for (int mt = 0; mt < 8; mt += RUN)
 #pragma unroll
-    for (int w = 0; w < kFewWarps; ++w) top = fmaxf(top, wm[w][tid]);
+      for (int r8 = 0; r8 < 2; ++r8) {
+        float* p = dst + M::vch(mt, r8, gr);
+        if constexpr (RUN == 2) {
+          *reinterpret_cast<float2*>(p) = f2(acc[mt][t][2 * r8], acc[mt + 1][t][2 * r8]);
+        } else {
 #pragma unroll
-    for (int w = 0; w < kFewWarps; ++w)
-      if (wl[w][tid] != 0.0f) l = fmaf(wl[w][tid], exp2_fast(wm[w][tid] - top), l);
-    a.part_s[part + (static_cast<size_t>(row0) + tid / a.g) * a.Hq + h * a.g + tid % a.g] = make_float2(top - kFewUp, l);
+          for (int i = 0; i < RUN; i += 4)
+            reinterpret_cast<float4*>(p)[i / 4] = make_float4(acc[mt + i][t][2 * r8], acc[mt + i + 1][t][2 * r8],
+                                                              acc[mt + i + 2][t][2 * r8], acc[mt + i + 3][t][2 * r8]);
+        }
+      }
   }
 }
 
@@ -1141,11 +1224,12 @@ Plan make_plan(const kvq_desc& d, int q_heads, int n_seqs, int n_rows, int max_r
   const long long tt = p.shared ? 2 * p.T : p.T;
   const long long by_rows = n_rows / tt + n_seqs, by_max = n_seqs * ((max_rows + tt - 1) / tt);
   p.tiles = p.few ? n_seqs : by_rows < by_max ? by_rows : by_max;
-  // about four CTAs per SM of 148 in turn, of at least 1024 keys each
+  // Few rows: eight CTAs an SM (four at a time), so that ragged sequences even out; 64 sequences of up
+  // to 8192 keys took 107 us with four an SM and 85 with eight, four of 32768 keys 43 and 45. Tiles: one
+  // CTA an SM, each with the query rows' set-up; 512 rows on 16384 keys took 222 us so and 269 with two.
   const long long all = p.tiles * heads, keys = max_kv > 0 ? max_kv : 1;
-  const long long tgt = getenv("TGT") ? atoi(getenv("TGT")) : 592, mk = getenv("MINK") ? atoi(getenv("MINK")) : 1024;
-  long long n = all > 0 ? tgt / all : 1;
-  const long long most = (keys + mk - 1) / mk;
+  long long n = all > 0 ? (p.few ? 8 : 1) * 148 / all : 1;
+  const long long most = (keys + 511) / 512;  // of at least 512 keys
   n = n < 1 ? 1 : n > most ? most : n;
   if (n > 256) n = 256;
   long long len = (keys + n - 1) / n;
@@ -1153,14 +1237,15 @@ Plan make_plan(const kvq_desc& d, int q_heads, int n_seqs, int n_rows, int max_r
   p.stretch = static_cast<int>(len > 0x40000000ll ? 0x40000000ll : len);
   p.n_stretch = static_cast<int>((keys + p.stretch - 1) / p.stretch);
   if (p.n_stretch < 1) p.n_stretch = 1;
-  p.n_parts = p.n_stretch * (p.shared || p.few ? 1 : 2);
+  p.n_parts = p.n_stretch * (p.few ? kFewWarps : p.shared ? 1 : 2);
   return p;
 }
 
 template <int D, int BITS, int G, bool SHARED>
 kvq_status run_tiles(const PagedArgs& a, long long grid, cudaStream_t st) {
   constexpr uint32_t smem = Cfg<D, SHARED>::kSmem;
-  if (!set_smem_once(reinterpret_cast<const void*>(k_paged_tiles<D, BITS, G, SHARED>), smem)) return KVQ_ERR_CUDA;
+  const void* fn = reinterpret_cast<const void*>(k_paged_tiles<D, BITS, G, SHARED>);
+  if (!set_smem_once(fn, smem) || !split_fits(fn, kRegsLaunch)) return KVQ_ERR_CUDA;
   k_paged_tiles<D, BITS, G, SHARED><<<static_cast<unsigned>(grid), kThreads, smem, st>>>(a);
   return launch_status();
 }
@@ -1168,9 +1253,28 @@ kvq_status run_tiles(const PagedArgs& a, long long grid, cudaStream_t st) {
 template <int BITS, int G, int NT>
 kvq_status run_few(const PagedArgs& a, long long grid, cudaStream_t st) {
   constexpr int smem = FewCfg<BITS, G>::kSmem;
-  static_assert(smem >= kFewWarps * 4 * NT * 128 * 4, "the ring holds the warps' sums at the end");
   if (!set_smem_once(reinterpret_cast<const void*>(k_paged_few<BITS, G, NT>), smem)) return KVQ_ERR_CUDA;
   k_paged_few<BITS, G, NT><<<static_cast<unsigned>(grid), kFewThreads, smem, st>>>(a);
+  return launch_status();
+}
+
+// Eight warps a row where there are more parts than one warp reads in one go.
+template <int D, int BITS, bool TILE>
+kvq_status run_merge(const PagedArgs& a, cudaStream_t st) {
+  const bool wide = a.n_parts > 8;
+  cudaLaunchConfig_t cfg{};
+  const long long warps = static_cast<long long>(a.n_rows) * a.Hq * (wide ? 8 : 1);
+  cfg.gridDim = dim3(static_cast<unsigned>((warps + 7) / 8));
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if ((wide ? cudaLaunchKernelEx(&cfg, k_paged_merge<D, BITS, TILE, 8>, a)
+            : cudaLaunchKernelEx(&cfg, k_paged_merge<D, BITS, TILE, 1>, a)) != cudaSuccess)
+    return KVQ_ERR_CUDA;
   return launch_status();
 }
 
@@ -1186,17 +1290,10 @@ kvq_status run(const PagedArgs& a, const Plan& p, cudaStream_t st) {
     s = p.shared ? run_tiles<D, BITS, G, true>(a, grid, st) : run_tiles<D, BITS, G, false>(a, grid, st);
   }
   if (s != KVQ_OK) return s;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>((static_cast<long long>(a.n_rows) * a.Hq + 7) / 8));
-  cfg.blockDim = dim3(256);
-  cfg.stream = st;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, k_paged_merge<D, BITS>, a) != cudaSuccess) return KVQ_ERR_CUDA;
-  return launch_status();
+  if constexpr (D == 128 && BITS != 3) {
+    if (p.few) return run_merge<D, BITS, false>(a, st);
+  }
+  return run_merge<D, BITS, true>(a, st);
 }
 
 size_t align256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
@@ -1233,8 +1330,8 @@ kvq_status launch_attend_paged(const kvq_desc& dk, const kvq_desc&, const void* 
   a.n_stretch = p.n_stretch;
   a.n_parts = p.n_parts;
   a.div_ps = FastDiv(static_cast<uint32_t>(dk.t_cap));
-  a.step_page = 128 / dk.t_cap;
-  a.step_off = 128 % dk.t_cap;
+  a.step_page = kFewStep / dk.t_cap;
+  a.step_off = kFewStep % dk.t_cap;
   a.q_stride = q_stride;
   a.out_stride = out_stride;
   a.scale = scale;

@@ -28,10 +28,19 @@ __device__ __forceinline__ void tmem_dealloc(uint32_t addr, uint32_t cols) {
 }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-// The mbarrier is arrived on when all products issued so far by this thread are done.
+// Products are issued by a whole warp in step, one elected lane doing it: with the warp together the
+// descriptors stay in uniform registers. In a branch of one lane the same instruction took 74 to 124
+// clocks to issue, whatever its size; so it takes 32 (N = 64) or 64 (N = 128), which is the tensor
+// cores' own rate. The mbarrier is arrived on when all products issued so far by this warp are done.
 __device__ __forceinline__ void tc_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-               : "memory");
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
+      : "memory");
+}
+// A wait of a whole warp: every lane has the same answer.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint64_t limit_ns, uint32_t* err) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, limit_ns, err));
 }
 
 #define KVQ_R4(a, i) "=r"(a[i]), "=r"(a[i + 1]), "=r"(a[i + 2]), "=r"(a[i + 3])
@@ -70,6 +79,12 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// Registers per thread of a warpgroup, every warp of which comes here.
+template <int N>
+__device__ __forceinline__ void more_regs() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void fewer_regs() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
 // ---------------------------------------------------------------- products
 // Shared-memory operand descriptor: start address, leading and stride byte
 // offsets (in 16-byte units), version 1, 128-byte swizzle. K-major: groups of
@@ -87,15 +102,15 @@ __host__ __device__ constexpr uint32_t mma_desc(int type, bool bt, int n) {
 }
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.u32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
       "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(acc))
       : "memory");
 }
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.u32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
       "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(acc))
       : "memory");
 }
@@ -129,7 +144,7 @@ __device__ __forceinline__ void issue_scores(uint32_t d, uint32_t a, uint32_t b)
 #pragma unroll
   for (int k = 0; k < D / 16; ++k) {
     const uint32_t off = (k / 4) * kTileBytes + (k % 4) * 32;
-    mma_ss(d, smem_desc(a + off, 16, 1024), smem_desc(b + off, 16, 1024), mma_desc(Elem<T>::kType, false, 128), k > 0);
+    mma_ss(d, smem_desc(a, 16, 1024) + (off >> 4), smem_desc(b, 16, 1024) + (off >> 4), mma_desc(Elem<T>::kType, false, 128), k > 0);
   }
 }
 // O[128 x D] (+)= P . V: P 128 x 128 16-bit in tensor memory, V 128 rows x D channels MN-major.
@@ -137,7 +152,7 @@ template <typename T, int D>
 __device__ __forceinline__ void issue_values(uint32_t o, uint32_t p, uint32_t v, bool acc) {
 #pragma unroll
   for (int k = 0; k < 8; ++k)
-    mma_ts(o, p + 8 * k, smem_desc(v + k * 2048, kTileBytes, 1024), mma_desc(Elem<T>::kType, true, D), acc || k > 0);
+    mma_ts(o, p + 8 * k, smem_desc(v, kTileBytes, 1024) + (k * 2048 >> 4), mma_desc(Elem<T>::kType, true, D), acc || k > 0);
 }
 
 // ---------------------------------------------------------------- softmax of a tile
@@ -261,13 +276,40 @@ struct RowItem {
   int q0;         // the tile's first row in the sequence
 };
 
-// Tile `idx` (of `tile` rows), counted from the last sequence's last tile backwards: under a causal
-// mask the long rows come first. One warp; item->len is 0 when there is no such tile. Offsets are cut
-// to [0, n_rows] and to ascending order.
+// Tile `idx` (of `tile` rows): under a causal mask a sequence's last tiles take longest and come first.
+// Up to 32 sequences: all sequences' tiles by their place in the sequence, from the last on. More: from
+// the last sequence's last tile backwards. One warp; item->len is 0 when there is no such tile. Offsets
+// are cut to [0, n_rows] and to ascending order.
 __device__ __forceinline__ void find_item(const int32_t* cu_rows, int n_seqs, int n_rows, int max_rows, int tile,
                                           int idx, int lane, RowItem* item) {
   if (lane == 0) item->len = 0;
   __syncwarp();
+  if (n_seqs <= 32) {
+    int b = 0, rows = 0;
+    if (lane < n_seqs) {
+      b = min(max(__ldg(cu_rows + lane), 0), n_rows);
+      rows = min(max(__ldg(cu_rows + lane + 1), b), n_rows) - b;
+    }
+    const int len = min(rows, max_rows), nt = (len + tile - 1) / tile;
+    // tiles at place p or behind it, over all sequences
+    auto behind = [&](int p) { return __reduce_add_sync(0xffffffffu, max(0, nt - p)); };
+    int lo = 0, hi = __reduce_max_sync(0xffffffffu, nt);
+    if (idx >= behind(0)) return;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (behind(mid) > idx) lo = mid; else hi = mid;
+    }
+    const int rank = idx - behind(lo + 1);
+    const uint32_t has = __ballot_sync(0xffffffffu, nt > lo);
+    if (nt > lo && __popc(has & ((1u << lane) - 1u)) == rank) {
+      item->seq = lane;
+      item->row0 = b;
+      item->rows = rows;
+      item->len = len;
+      item->q0 = lo * tile;
+    }
+    return;
+  }
   for (int s0 = n_seqs - 1; s0 >= 0; s0 -= 32) {
     const int s = s0 - lane;
     int b = 0, rows = 0;

@@ -151,6 +151,19 @@ inline int occupancy_once(const void* fn, int threads, size_t smem) {
   return per_sm;
 }
 
+// Whether a kernel that divides its registers anew after launch was built with the registers that the
+// division counts on (fewer, and it would wait for ever). Asked once per kernel and thread.
+inline bool split_fits(const void* fn, int regs) {
+  static thread_local const void* known[64];
+  static thread_local int n = 0;
+  for (int i = 0; i < n; ++i)
+    if (known[i] == fn) return true;
+  cudaFuncAttributes a;
+  if (cudaFuncGetAttributes(&a, fn) != cudaSuccess || a.numRegs < regs) return false;
+  if (n < 64) known[n++] = fn;
+  return true;
+}
+
 // Finish a launch: map a launch error to a status.
 inline kvq_status launch_status() {
   return cudaGetLastError() == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;

@@ -42,10 +42,12 @@ __device__ __forceinline__ int sat32(long long v) { return v > 0x7fffffffll ? 0x
 __device__ __forceinline__ void seq_pages(const MapArgs& a, int s, int& ctx, int& n, int& k0, int& need) {
   ctx = max(0, __ldg(a.ctx_len + s));
   n = max(0, __ldg(a.new_len + s));
-  const long long ps = a.div_ps.d;
-  k0 = static_cast<int>((ctx + ps - 1) / ps);
-  const long long k1 = (static_cast<long long>(ctx) + n + ps - 1) / ps;
-  need = static_cast<int>(max(0ll, min(k1, static_cast<long long>(a.max_pages)) - k0));
+  auto pages = [&](int tokens) {  // rounded up
+    const uint32_t t = static_cast<uint32_t>(tokens), q = a.div_ps.div(t);
+    return static_cast<int>(q + (a.div_ps.mod(t, q) != 0));
+  };
+  k0 = pages(ctx);
+  need = max(0, min(pages(sat32(static_cast<long long>(ctx) + n)), a.max_pages) - k0);
 }
 
 // Largest s in [0, S) with off[s] <= v (off ascending, off[0] <= v < off[S]).
