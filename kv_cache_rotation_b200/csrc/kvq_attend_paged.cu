@@ -356,9 +356,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_tiles(const PagedArgs a) 
       const uint32_t seen[4] = {bits.x & first_bits(left, 0), bits.y & first_bits(left, 32),
                                 bits.z & first_bits(left, 64), bits.w & first_bits(left, 96)};
       if (__all_sync(0xffffffffu, (seen[0] & seen[1] & seen[2] & seen[3]) == 0xffffffffu))
-        softmax_tile<__half, D, false, true>(s_addr, o_addr, i > 0, mul, st, seen);
+        softmax_tile<__half, D, false>(s_addr, o_addr, i > 0, mul, st, seen);
       else
-        softmax_tile<__half, D, true, true>(s_addr, o_addr, i > 0, mul, st, seen);
+        softmax_tile<__half, D, true>(s_addr, o_addr, i > 0, mul, st, seen);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&m->p_full[t]);

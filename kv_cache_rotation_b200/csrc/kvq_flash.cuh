@@ -182,47 +182,28 @@ __device__ __forceinline__ uint32_t first_bits(int left, int at) {
 // reference rises. Warp-uniform: every lane of the warp calls it. Each weight
 // is rounded once to T for the product (relative 2^-12 on average in fp16,
 // 2^-9 in bf16, where a sum over many keys averages it out); the row sum takes
-// the unrounded weights. HOLD keeps the row's 128 scores in registers between
-// the maximum and the weights; without it they are read twice.
-template <typename T, int D, bool MASKED, bool HOLD>
+// the unrounded weights. The row's 128 scores stay in registers between the
+// maximum and the weights: reading them twice, or two threads to a row, was
+// slower (562 against 529 us for 16384 tokens of 8 / 2 heads of 128).
+template <typename T, int D, bool MASKED>
 __device__ __forceinline__ void softmax_tile(uint32_t s_addr, uint32_t o_addr, bool have_o, float mul, RowStat& st,
                                              const uint32_t (&seen)[4]) {
-  uint32_t r[HOLD ? 128 : 32];
-  auto load = [&](int c, uint32_t* x) {
-    tmem_ld32(s_addr + 32 * c, x);
-    tmem_wait_ld32(x);
-  };
-  auto mask = [&](int c, uint32_t* x) {
-    if constexpr (MASKED) {
-      uint32_t b = seen[c];
-      asm volatile("" : "+r"(b));  // the 128 tests are not kept from the first reading for the second
-#pragma unroll
-      for (int i = 0; i < 32; ++i) x[i] = (b >> i) & 1u ? x[i] : 0xff800000u;
-    }
-  };
+  uint32_t r[128];
   float mx = -INFINITY, mx2 = -INFINITY;
-  auto top = [&](const uint32_t* x) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c) tmem_ld32(s_addr + 32 * c, r + 32 * c);
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    uint32_t* x = r + 32 * c;
+    tmem_wait_ld32(x);
+    if constexpr (MASKED) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) x[i] = (seen[c] >> i) & 1u ? x[i] : 0xff800000u;
+    }
 #pragma unroll
     for (int i = 0; i < 32; i += 4) {
       mx = max3f(mx, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
       mx2 = max3f(mx2, __uint_as_float(x[i + 2]), __uint_as_float(x[i + 3]));
-    }
-  };
-  if constexpr (HOLD) {
-#pragma unroll
-    for (int c = 0; c < 4; ++c) tmem_ld32(s_addr + 32 * c, r + 32 * c);
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      tmem_wait_ld32(r + 32 * c);
-      mask(c, r + 32 * c);
-      top(r + 32 * c);
-    }
-  } else {
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      load(c, r);
-      mask(c, r);
-      top(r);
     }
   }
   mx = fmaxf(mx, mx2) * mul;
@@ -249,11 +230,7 @@ __device__ __forceinline__ void softmax_tile(uint32_t s_addr, uint32_t o_addr, b
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
     uint32_t w[16];
-    uint32_t* x32 = r + (HOLD ? 32 * c : 0);
-    if constexpr (!HOLD) {
-      load(c, x32);
-      mask(c, x32);
-    }
+    const uint32_t* x32 = r + 32 * c;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       const float2 x = fma2(f2(__uint_as_float(x32[2 * i]), __uint_as_float(x32[2 * i + 1])), mul2v, nm2);

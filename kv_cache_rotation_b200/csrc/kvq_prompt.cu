@@ -133,9 +133,9 @@ __global__ void __launch_bounds__(Split<SLOTS>::kThreads, 3 - SLOTS)
       const int left = lim - 128 * i;  // columns seen
       const uint32_t seen[4] = {first_bits(left, 0), first_bits(left, 32), first_bits(left, 64), first_bits(left, 96)};
       if (__any_sync(0xffffffffu, left < 128))
-        softmax_tile<T, D, true, true>(s_addr, o_addr, i > 0, a.mul, st, seen);
+        softmax_tile<T, D, true>(s_addr, o_addr, i > 0, a.mul, st, seen);
       else
-        softmax_tile<T, D, false, true>(s_addr, o_addr, i > 0, a.mul, st, seen);
+        softmax_tile<T, D, false>(s_addr, o_addr, i > 0, a.mul, st, seen);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&m->p_full[t]);
