@@ -340,7 +340,8 @@ kvq_status kvq_decode_paged(const kvq_desc* d, const kvq_packed* in, const kvq_p
  *   workspace  kvq_attend_paged_workspace_bytes() bytes, 256-byte aligned, contents irrelevant, not
  *            shared by calls in flight at the same time
  * Scores, softmax statistics and sums are held in fp32; the decoded keys and values and the softmax
- * weights enter the products rounded to fp16, sinks enter in fp32. */
+ * weights enter the products rounded to fp16, sinks enter in fp32. A record of infinite or NaN values
+ * leaves the rows that see it without a usable result and has no effect on the others. */
 kvq_status kvq_attend_paged(const kvq_desc* dk, const kvq_desc* dv, const void* q, int64_t q_stride, int32_t q_heads,
                             const kvq_packed* k_cache, const kvq_tables* tk, const kvq_packed* v_cache,
                             const kvq_tables* tv, const kvq_paged* pg, int32_t max_rows, int32_t max_kv, float scale,

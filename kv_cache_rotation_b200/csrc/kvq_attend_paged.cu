@@ -161,6 +161,20 @@ struct Record {
 #pragma unroll
     for (int i = 0; i < kSz; ++i) sz[i] = __ldg(z + i);
   }
+  // Whether a channel can be infinite or NaN as fp16; the record becomes zero then.
+  __device__ __forceinline__ bool clear_if_bad() {
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < kSz; ++i) {
+      const float2 z = __half22float2(*reinterpret_cast<const __half2*>(&sz[i]));
+      bad |= !(fabsf(z.y) < 65520.0f && fabsf(fmaf(static_cast<float>((1 << BITS) - 1), z.x, z.y)) < 65520.0f);
+    }
+    if (bad) {
+#pragma unroll
+      for (int i = 0; i < kSz; ++i) sz[i] = 0;
+    }
+    return bad;
+  }
   // Row r of a tile as fp16: the eight lanes of a store phase have eight rows, so the swizzle sends
   // them to eight bank groups.
   __device__ __forceinline__ void store(uint32_t tile, int r) const {
@@ -194,6 +208,7 @@ struct Cfg {
 struct Misc {
   uint64_t first[2], full[2], empty[2], s_full[2], p_full[2], o_full[2], begun, drain;
   uint32_t tmem;
+  int bad;  // first position of a value record that is not finite, among those that some row does not see
   RowItem item;
   alignas(16) uint32_t seen[kMasks][4];  // read 16 bytes at a time
   float mul[2][128];
@@ -272,6 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_tiles(const PagedArgs a) 
       mbar_init(&m->p_full[i], SHARED ? 4 : live_warps);
     }
     mbar_init(&m->begun, 1), mbar_init(&m->drain, 1);
+    m->bad = 0x7fffffff;
     fence_mbar_init();
   }
   // the query rows, rotated, scaled by a power of two into [1, 2) and rounded once to fp16
@@ -367,6 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_tiles(const PagedArgs a) 
     if (ok && works) {
       const size_t at = static_cast<size_t>(SHARED ? z : 2 * z + t) * (static_cast<size_t>(a.n_rows) * a.Hq) +
                         (static_cast<size_t>(it.row0) + it.q0 + tok) * a.Hq + h * a.g + j;
+      if (nt > 0 && *reinterpret_cast<volatile int*>(&m->bad) < lim) st.l = NAN;
       if (mine) a.part_s[at] = make_float2(st.m, st.l);
       if (nt > 0) {
         tc_fence_after();
@@ -438,6 +455,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_tiles(const PagedArgs a) 
       if (j >= 2) ok = warp_wait(&m->empty[s], ((j >> 1) & 1) ^ 1, a.wait_ns, a.err);
       if (ok && j == 2 - A) ok = warp_wait(&m->begun, 0, a.wait_ns, a.err);  // K_2 takes the place of K_0
       if (!ok) break;
+      // a weight of zero does not hide what is not finite: where some row does not see a key (behind the first
+      // token's), such a record is taken out, and the rows that see it get a total of NaN
+      if (k0 + 128 * j + 127 > pos0 && vr.clear_if_bad()) atomicMin(&m->bad, k0 + 128 * j + r);
       vr.store(vs + s * C::kHead, r);
       vp = v2;
       v2 = A == 1 ? kn : kp;
@@ -572,11 +592,19 @@ __global__ void __launch_bounds__(256) k_paged_merge(const PagedArgs a) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, w = warp % W;
   const long long wi = (blockIdx.x * 8ll + warp) / W;
   const int row = static_cast<int>(wi / a.Hq), qh = static_cast<int>(wi % a.Hq);
-  if (row >= a.n_rows) return;  // the W warps of a row agree, here and below
+  // Every path waits for the tiles' grid: a kernel behind this one counts on both being done.
+  auto after_tiles = [] { asm volatile("griddepcontrol.wait;" ::: "memory"); };
+  if (row >= a.n_rows) {  // the W warps of a row agree, here and below
+    after_tiles();
+    return;
+  }
   const int lo = seq_of_row(a.cu_rows, a.S, row, lane);
   const int b = min(max(__ldg(a.cu_rows + lo), 0), a.n_rows), e = min(max(__ldg(a.cu_rows + lo + 1), b), a.n_rows);
   const int h = qh / a.g, len = max(__ldg(a.kv_len + lo), 0);
-  if (row < b || row >= e || row - b >= a.max_rows) return;
+  if (row < b || row >= e || row - b >= a.max_rows) {
+    after_tiles();
+    return;
+  }
   // keys [0, lim)
   const int lim = min(len - (e - b) + (row - b) + 1, min(len, sat_pages(a.max_pages, static_cast<int>(a.div_ps.d))));
   const float unit = a.scale * 1.4426950408889634f;
@@ -629,7 +657,7 @@ __global__ void __launch_bounds__(256) k_paged_merge(const PagedArgs a) {
       }
     }
   }
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  after_tiles();
   // the stretches that hold keys of this row, an empty part (weight total 0) left out
   const size_t rows = static_cast<size_t>(a.n_rows) * a.Hq, me = static_cast<size_t>(row) * a.Hq + qh;
   const int per = a.n_parts / a.n_stretch;
@@ -870,7 +898,7 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 4 : 2) k_paged_few(cons
   if (tokens == 0 || k1 <= k0) return;  // no row sees a key here: the merge does not look
   const int n_rows = tokens * a.g;      // at most R
   const int blocks = (k1 - k0 + kBlock - 1) / kBlock;
-  const int mine = blocks > warp ? (blocks - warp + kFewWarps - 1) / kFewWarps : 0;  // blocks warp + 8 i
+  const int mine = blocks > warp ? (blocks - warp + kFewWarps - 1) / kFewWarps : 0;  // blocks warp + kFewWarps i
 
   // ---- the ring: lane copies half a record of key lane / 2, and its (S, Z) (even lanes keys, odd lanes values)
   const uint32_t wbase = smem_u32(few_smem) + warp * (ST * C::kStage);
@@ -1022,7 +1050,7 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 4 : 2) k_paged_few(cons
   const uint32_t sel = (gr & 1) ? 0x7632u : 0x5410u;
 
   uint32_t stage = 0;
-  int n0 = k0 + warp * kBlock;
+  int n0 = k0 + warp * kBlock, bad = 0x7fffffff;  // the first value record met that is not finite, see below
   for (int i = 0; i < mine; ++i, n0 += kFewStep) {
     cp_async_wait_group<ST - 1>();
     __syncwarp();
@@ -1061,6 +1089,21 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 4 : 2) k_paged_few(cons
       va[k] = *reinterpret_cast<const uint32_t*>(sz + ((2 * gr + 1) * NG + k) * 4);
       vb[k] = *reinterpret_cast<const uint32_t*>(sz + ((2 * (gr + 8) + 1) * NG + k) * 4);
     }
+    // A weight of zero does not hide what is not finite: in the blocks with keys that some row does not see,
+    // such a record is taken out, and the rows that see it get a total of NaN.
+    if (n0 + kBlock > pos0 + 1) {
+      auto clear = [&](uint32_t (&z)[NG], int key) {
+        bool out = false;
+#pragma unroll
+        for (int k = 0; k < NG; ++k) out |= (z[k] & 0x7c00u) == 0x7c00u || (z[k] & 0x7c000000u) == 0x7c000000u;
+        if (!out) return;
+#pragma unroll
+        for (int k = 0; k < NG; ++k) z[k] = 0;
+        bad = min(bad, key);
+      };
+      clear(va, n0 + gr);
+      clear(vb, n0 + gr + 8);
+    }
     // log2 of the largest value scale of each key, for the range of its weights
     float ta = kFewMinS, tb = kFewMinS;
     float2 va2[NG], vb2[NG];
@@ -1068,8 +1111,8 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 4 : 2) k_paged_few(cons
     for (int k = 0; k < NG; ++k) {
       va2[k] = h2f2(va[k]);
       vb2[k] = h2f2(vb[k]);
-      ta = fmaxf(ta, va2[k].x);
-      tb = fmaxf(tb, vb2[k].x);
+      ta = fmaxf(ta, fabsf(va2[k].x));
+      tb = fmaxf(tb, fabsf(vb2[k].x));
     }
     float lga, lgb;
     asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(lga) : "f"(ta));
@@ -1170,6 +1213,7 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 4 : 2) k_paged_few(cons
   const size_t part = static_cast<size_t>(z * kFewWarps + warp) * (static_cast<size_t>(a.n_rows) * a.Hq);
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
+    if (bad < lim[t]) lr[t] = NAN;
 #pragma unroll
     for (int o = 4; o < 32; o <<= 1) {
       lr[t] += __shfl_xor_sync(0xffffffffu, lr[t], o);

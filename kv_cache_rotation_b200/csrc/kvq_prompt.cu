@@ -185,7 +185,8 @@ __global__ void __launch_bounds__(Split<SLOTS>::kThreads, 3 - SLOTS)
         for (int c = 0; c < D / 64; ++c)
           tma_load_3d(gbase + t * C::kHead + c * kTileBytes, &mq, 64 * c, h * a.g, row0 + q0 + t * a.T, &m->q_full);
       // V from the diagonal on lands on a barrier of its own, used once: its cleaners have not followed the ring's
-      // phases. No stage is used again behind such a tile (at most three of them, five stages).
+      // phases. No other load follows on such a stage (two or four stages: only V, each on its own barrier;
+      // five or ten: at most three such tiles, so the call's last load comes sooner).
       auto landed = [&](int i) {
         return (i & 1) && (i >> 1) >= edge ? &m->loaded[(i >> 1) - edge] : &m->full[i % ST];
       };

@@ -77,20 +77,3 @@ def softmax_rows(s, seen):
     p = np.where(seen, p, 0.0)
     total = p.sum(-1, keepdims=True)
     return p / np.where(total > 0, total, 1.0)
-
-
-def attend_bound(q, k, v, p, scale, u_qk, u_p, u_v, u_out, out):
-    """Per-element bound of an attention output: q [m, D], k, v [n, D] (the bases in which the
-    products run), p [m, n] the exact weights. Every operand of the scores is off by at most u_qk
-    relative (0 where it enters as it is), so a score by e = scale sum |q||k| ((1 + u_qk)^2 - 1) plus
-    fp32 sums of D products (D 2^-23 of the same sum: a tensor-core sum may truncate); a weight by
-    e^(2e) - 1 of itself, exp's own error (2^-21, its argument below 2^4 in base 2 near the weights
-    that count) and its rounding u_p; the values by u_v; the row sum of l weights by n 2^-24; the
-    fp32 sum over the keys by n 2^-23; the result by u_out. A rotation of the result keeps the
-    2-norm of the error, so the bound is the 2-norm over the channels where the product runs in
-    another basis; it is used for every channel."""
-    mag = scale * (np.abs(q) @ np.abs(k).T)
-    e = (mag * ((1 + u_qk) ** 2 - 1 + q.shape[1] * 2.0 ** -23)).max(-1, where=p > 0, initial=0.0)[:, None]
-    rel = np.expm1(2 * e) + 2.0 ** -20 + u_p + u_v + k.shape[0] * 2.0 ** -22
-    err = (p @ np.abs(v)) * rel
-    return np.linalg.norm(err, axis=-1, keepdims=True) + u_out * np.abs(out) + 2.0 ** -24

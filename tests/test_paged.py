@@ -485,6 +485,32 @@ def test_attend_paged_rows_that_see_nothing():
 
 
 @gpu
+@pytest.mark.parametrize("which", [0, 1], ids=["keys", "values"])
+@pytest.mark.parametrize("S,Z", [(0x7c00, 0x3c00), (0x3c00, 0xfc00), (0x7e00, 0x7e00), (0x7bff, 0x7bff)],
+                         ids=["scale inf", "zero -inf", "nan", "sum too large"])
+@pytest.mark.parametrize("new,at,Hq,bits,group", [
+    ([3, 2], 1, 2, 2, 128), ([4, 4], 3, 4, 4, 32), ([3, 1], 2, 4, 2, 64),   # few rows: one tile and two
+    ([20, 4], 11, 8, 2, 128), ([32, 1], 31, 8, 3, 32),                      # one slot of rows
+    ([200, 70], 130, 8, 4, 64), ([300, 9], 40, 4, 2, 128),                  # two, and more than one tile of rows
+])
+def test_attend_paged_later_records_that_are_not_finite(new, at, Hq, bits, group, S, Z, which):
+    """A later token's record has no effect on a row, whatever it holds."""
+    t = Attend([100, 60], new, Hq, 2, 128, bits, group, 0, False, 0, "fwht_head", 16, extra=2)
+    t.call()()
+    clean = t.out.clone()
+    pos = 100 + at
+    sz = t.packs[which].scale_zero
+    sz[t.b.m["block_table"][0][pos // 16], :, pos % 16] = torch.tensor([S, Z], dtype=torch.int32).to(torch.int16).cuda()
+    t.out.fill_(7.0)
+    t.call()()
+    assert K.kvq_check(0) == OK
+    assert torch.equal(t.out[:at], clean[:at]) and torch.equal(t.out[new[0]:], clean[new[0]:])
+    # an infinite key may have the score -inf and so no weight; a large finite scale is a value in fp32
+    if S == 0x7e00 or (which == 1 and S != 0x7bff):
+        assert not torch.isfinite(t.out[at:new[0]]).all(-1).any()
+
+
+@gpu
 def test_attend_paged_bad_lengths_stay_in_bounds():
     t = Attend([40, 60], [8, 1], 8, 2, 128, 2, 128, 1, False, 4, "fwht_head", 16)
     for cu, kv in (([0, 1 << 30, 9], [48, 61]), ([-4, 8, 9], [48, 61]), ([9, 8, 0], [48, 61]),
