@@ -14,8 +14,13 @@
 // prompt: SHARED), or the same rows with alternate tiles of keys (up to 128 rows,
 // a decode step: the second slot is then half of the stretch). Each slot leaves
 // its sums, reference and weight total per row in the workspace.
-// k_paged_merge: one warp per row and query head joins them with the sinks and
-// turns the result back.
+// k_paged_merge: a warp, or eight, per row and query head joins them with the sinks
+// and turns the result back.
+//
+// Measured, 32 / 8 heads of 128: 512 rows on 16384 keys of 4 bits 215 us = 650 TFLOP/s
+// (40 % of the products' rate): a slot's softmax of a tile, 2400 to 2800 clocks beside
+// the record warps, and its products take turns; tensor pipe 39 %, exponentials 40 %.
+// Twelve sequences of 1 to 131 rows on up to 8000 keys of 3 bits 205 us.
 #include <math.h>
 
 #include "kvq_flash.cuh"
@@ -25,7 +30,7 @@ namespace kvq {
 namespace {
 
 constexpr int kProdWarps = 4;
-constexpr int kThreads = 512;  // warps 0-7 softmax, 8-11 records, 12 products, the rest idle
+constexpr int kThreads = 512;  // warps 0-7 softmax, 8-11 records, 12 products; 13-15 only help with the query rows
 // Registers a thread has at launch (the launch bound's limit), and after the split by warpgroup. A sum
 // above the launch's would wait for ever.
 constexpr int kRegsLaunch = 128, kRegsSoftmax = 200, kRegsRecords = 88, kRegsIssue = 24;
@@ -757,6 +762,10 @@ __global__ void __launch_bounds__(256) k_paged_merge(const PagedArgs a) {
 //           (A = 16 channels x 16 keys of codes, B = weights)
 // A weight p S is at most 2^15: the reference m follows s + log2 S (S >= 2^-30)
 // and is raised when that exceeds it by 2^8; p = 2^(s - m + 7).
+//
+// Measured, 2 bits, one group, 32 / 8 heads: 64 sequences of up to 8191 keys 85 us (159
+// MB, 1.9 TB/s), four of 32768 keys 45 us. 271 instructions per 16 keys and warp, about
+// 80 of them masks and shifts of codes: ALU pipe 52 %, issue 55 %, DRAM 26 %.
 constexpr int kFewWarps = 4;
 constexpr int kFewThreads = 32 * kFewWarps;
 constexpr int kBlock = 16;

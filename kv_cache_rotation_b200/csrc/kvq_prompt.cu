@@ -15,6 +15,11 @@
 // Warps: 0-3 and 4-7 softmax of slots 0 and 1; 8 loads; 9 issues the products;
 // 10 and 11 clear what the mask hides in V (see below).
 //
+// Measured: 16384 tokens of 8 / 2 heads of 128, bf16, 521 us = 1055 TFLOP/s, at the
+// power limit (1.37 GHz; tensor pipe and exponentials 51 % each, in turn). Nine
+// prompts, 6500 tokens, 32 / 8 heads, 122 us: set-up and epilogue of a CTA (about 5500
+// clocks) and a short grid's tail. One prompt of 77 tokens 8.5 us: a launch and one chain.
+//
 // Masked keys get weight 0, but 0 * inf is not 0, so V must be finite wherever
 // a weight is masked: only the last tiles of a CTA (from the diagonal on) hold
 // masked keys, and two warps go over those: rows behind the sequence become
