@@ -200,13 +200,21 @@ struct Record {
   }
 };
 
+constexpr int kOutPitch = 20;  // words: eight rows' 16-byte pieces meet all banks
 template <int D, bool SHARED>
 struct Cfg {
   static constexpr uint32_t kHead = D / 64 * kTileBytes;
   static constexpr uint32_t kK = (SHARED ? 2 : 1) * kHead;  // two stages of keys behind the query rows
   static constexpr uint32_t kV = kK + 2 * kHead;
   static constexpr uint32_t kMisc = kV + 2 * kHead;
-  static constexpr uint32_t kSmem = kMisc + 2048 + 1024;
+  // The sums on their way out, 32 rows x 16 channels of each softmax warp: over the slot's own query rows,
+  // which nothing reads any more then, or (slots that share them) behind the rest. What shared memory does
+  // not take is L1, where the records' lines wait for a thread's next 16 bytes: with 20 KB less of it a
+  // tile took 4950 clocks, not 4370.
+  static constexpr uint32_t kOutWarp = 32 * kOutPitch * 4;
+  static constexpr uint32_t kOut = SHARED ? 0 : kMisc + 2048, kOutSlot = SHARED ? kHead : 4 * kOutWarp;
+  static_assert(4 * kOutWarp <= kHead, "over the query rows");
+  static constexpr uint32_t kSmem = kMisc + 2048 + (SHARED ? 0 : 8 * kOutWarp) + 1024;
   static constexpr int kAhead = SHARED ? 1 : 2;  // tiles of keys before the first tile of values
 };
 
@@ -295,48 +303,109 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_tiles(const PagedArgs a) 
     m->bad = 0x7fffffff;
     fence_mbar_init();
   }
-  // the query rows, rotated, scaled by a power of two into [1, 2) and rounded once to fp16
+  // The query rows, rotated, scaled by a power of two into [1, 2) and rounded once to fp16: two lanes a
+  // row, lane `half` with every other chunk of 8 channels, so all strides but 8 stay in registers. (With a
+  // warp a row the shuffles alone took 13000 clocks for 256 rows, the set-up 21700 of a CTA's 320000.)
   {
-    constexpr int CH = D / 32, AT = 4, WARPS = kThreads / 32;  // four rows of a warp on their way at a time
-    int ch[CH];
+    constexpr int NC = D / 16;  // chunks of a lane: 2k + half
+    const int rr = tid >> 1, half = tid & 1, t = rr >> 7, tr = rr & 127;
+    const int tk = tr / a.g, tok = t * a.T + tk, j = tr - tk * a.g;
+    const bool mine = t < SLOTS && tk < a.T && tok < tokens;
+    if (__any_sync(0xffffffffu, mine)) {
+      const __half* qp = a.q + (static_cast<int64_t>(it.row0) + it.q0 + (mine ? tok : 0)) * a.q_stride + (h * a.g + (mine ? j : 0)) * D;
+      uint4 raw[NC];
 #pragma unroll
-    for (int c = 0; c < CH; ++c) ch[c] = a.kperm ? a.kperm[h * D + lane * CH + c] & (D - 1) : lane * CH + c;
-    const int rows = tokens * a.g;
-    for (int r0 = warp; r0 < rows; r0 += AT * WARPS) {
-      __half raw[AT][CH];
+      for (int k = 0; k < NC; ++k) raw[k] = __ldg(reinterpret_cast<const uint4*>(qp) + 2 * k + half);
+      if (a.kperm) {  // through a copy of the row where the keys will be
+        uint32_t* const buf = reinterpret_cast<uint32_t*>(gbase + C::kK) + rr * (D / 2 + 1);
 #pragma unroll
-      for (int k = 0; k < AT; ++k) {
-        const int r = min(r0 + k * WARPS, rows - 1), tok = r / a.g, j = r - tok * a.g;
-        const __half* qp = a.q + (static_cast<int64_t>(it.row0) + it.q0 + tok) * a.q_stride + (h * a.g + j) * D;
+        for (int k = 0; k < NC; ++k) {
+          uint32_t* b = buf + 4 * (2 * k + half);
+          b[0] = raw[k].x, b[1] = raw[k].y, b[2] = raw[k].z, b[3] = raw[k].w;
+        }
+        __syncwarp();
+        const uint16_t* row = reinterpret_cast<const uint16_t*>(buf);
 #pragma unroll
-        for (int c = 0; c < CH; ++c) raw[k][c] = __ldg(qp + ch[c]);
+        for (int k = 0; k < NC; ++k) {
+          const uint4 pm = __ldg(reinterpret_cast<const uint4*>(a.kperm + h * D) + 2 * k + half);
+          auto two = [&](uint32_t w) {
+            return static_cast<uint32_t>(row[w & (D - 1)]) | (static_cast<uint32_t>(row[(w >> 16) & (D - 1)]) << 16);
+          };
+          raw[k] = make_uint4(two(pm.x), two(pm.y), two(pm.z), two(pm.w));
+        }
+        __syncwarp();
+      }
+      float x[NC][8];
+#pragma unroll
+      for (int k = 0; k < NC; ++k) h8_to_f32(raw[k], x[k]);
+      // the partner's half of a chunk pair comes over, this lane's other half goes: then it has channels
+      // 16 k + e and 16 k + 8 + e for four e, of the codes' order of channels
+      constexpr bool kBy2 = BITS == 4;  // e = 2 half + {0, 1, 4, 5}; else 4 half + {0 .. 3}
+      float top = 0.0f;
+#pragma unroll
+      for (int k = 0; k < NC; ++k) {
+        if (a.rot) fwht_reg<8>(x[k]);
+        float y[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int lo = kBy2 ? (i & 1) + 4 * (i >> 1) : i, hi = lo + (kBy2 ? 2 : 4);
+          const float keep = half ? x[k][hi] : x[k][lo], give = half ? x[k][lo] : x[k][hi];
+          const float got = __shfl_xor_sync(0xffffffffu, give, 1);
+          const float a0 = half ? got : keep, a1 = half ? keep : got;  // channel 16 k + e, and 8 further
+          y[i] = a.rot ? a0 + a1 : a0;
+          y[4 + i] = a.rot ? a0 - a1 : a1;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[k][i] = y[i];
+      }
+      if (a.rot) {
+#pragma unroll
+        for (int o = 1; o < NC; o <<= 1)
+#pragma unroll
+          for (int k = 0; k < NC; ++k)
+            if ((k & o) == 0)
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const float u = x[k][i], v = x[k + o][i];
+                x[k][i] = u + v;
+                x[k + o][i] = u - v;
+              }
+#pragma unroll
+        for (int k = 0; k < NC; ++k)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[k][i] *= a.rscale;
       }
 #pragma unroll
-      for (int k = 0; k < AT; ++k) {
-        const int r = r0 + k * WARPS;
-        if (r >= rows) break;
-        const int tok = r / a.g, t = tok / a.T, tr = r - t * a.T * a.g;
-        float x[CH];
+      for (int k = 0; k < NC; ++k)
 #pragma unroll
-        for (int c = 0; c < CH; ++c) x[c] = __half2float(raw[k][c]);
-        if (a.rot) {
-          warp_fwht<CH>(x, lane);
+        for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[k][i]));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      const int e = top > 0.0f && top < INFINITY ? static_cast<int>(__float_as_uint(top) >> 23) - 127 : 0;
+      const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+      if (mine) {
+        uint8_t* const tile = gbase + t * C::kHead;
+        auto at = [&](int p) { return tile + (p / 64) * kTileBytes + sw128(tr, (p % 64) / 8) + 2 * (p % 8); };
+        using E = Elem<__half>;
 #pragma unroll
-          for (int c = 0; c < CH; ++c) x[c] *= a.rscale;
+        for (int k = 0; k < NC; ++k) {
+          float (&y)[8] = x[k];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) y[i] *= down;
+          if constexpr (BITS == 2) {  // 16 k + 2 e, + 1
+            *reinterpret_cast<uint4*>(at(16 * k + 8 * half)) =
+                make_uint4(E::pack(y[0], y[4]), E::pack(y[1], y[5]), E::pack(y[2], y[6]), E::pack(y[3], y[7]));
+          } else if constexpr (BITS == 4) {  // 16 k + 2 (e & 3) + (e >> 2), and 8 further
+            *reinterpret_cast<uint2*>(at(16 * k + 4 * half)) = make_uint2(E::pack(y[0], y[2]), E::pack(y[1], y[3]));
+            *reinterpret_cast<uint2*>(at(16 * k + 8 + 4 * half)) = make_uint2(E::pack(y[4], y[6]), E::pack(y[5], y[7]));
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int ch = 16 * k + 8 * (i >> 2) + (i & 3), p = half ? tile_pos<BITS>(ch + 4) : tile_pos<BITS>(ch);
+              *reinterpret_cast<__half*>(at(p)) = __float2half_rn(y[i]);
+            }
+          }
         }
-        float top = 0.0f;
-#pragma unroll
-        for (int c = 0; c < CH; ++c) top = fmaxf(top, fabsf(x[c]));
-        top = all_max(top);
-        const int e = top > 0.0f && top < INFINITY ? static_cast<int>(__float_as_uint(top) >> 23) - 127 : 0;
-        const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-#pragma unroll
-        for (int c = 0; c < CH; ++c) {
-          const int p = tile_pos<BITS>(lane * CH + c);
-          *reinterpret_cast<__half*>(gbase + t * C::kHead + (p / 64) * kTileBytes + sw128(tr, (p % 64) / 8) + 2 * (p % 8)) =
-              __float2half_rn(x[c] * down);
-        }
-        if (lane == 0) m->mul[t][tr] = a.scale * 1.4426950408889634f * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+        if (half == 0) m->mul[t][tr] = a.scale * 1.4426950408889634f * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
       }
     }
     fence_async_smem();
@@ -356,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_tiles(const PagedArgs a) 
   if (warp < 8) {
     more_regs<kRegsSoftmax>();
     const int t = warp >> 2, tq = SHARED ? t : 0;
-    const int r = tid & 127, tok = tq * a.T + r / a.g, j = r % a.g;
+    const int r = tid & 127, tok = tq * a.T + r / a.g;
     const bool mine = r < a.T * a.g && tok < tokens;
     const int lim = mine ? pos0 + tok + 1 : 0x7fffffff;
     const float mul = mine ? m->mul[tq][r] : 0.0f;
@@ -386,21 +455,44 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_tiles(const PagedArgs a) 
     }
     if (ok && nt > 0) ok = warp_wait(&m->o_full[t], 0, a.wait_ns, a.err);
     if (ok && works) {
-      const size_t at = static_cast<size_t>(SHARED ? z : 2 * z + t) * (static_cast<size_t>(a.n_rows) * a.Hq) +
-                        (static_cast<size_t>(it.row0) + it.q0 + tok) * a.Hq + h * a.g + j;
+      // rows of a KV head in the order of the packed rows: row i of the warp's 32 is at first + i / g * Hq + i % g
+      int rw = r & ~31;
+      asm volatile("" : "+r"(rw));  // nothing of this is worked out before the loop and kept in registers
+      const size_t part = static_cast<size_t>(SHARED ? z : 2 * z + t) * (static_cast<size_t>(a.n_rows) * a.Hq) + h * a.g;
+      const int rt = (rw + lane) / a.g;
+      const size_t at = part + (static_cast<size_t>(it.row0) + it.q0 + tq * a.T + rt) * a.Hq + (rw + lane - rt * a.g);
       if (nt > 0 && *reinterpret_cast<volatile int*>(&m->bad) < lim) st.l = NAN;
       if (mine) a.part_s[at] = make_float2(st.m, st.l);
       if (nt > 0) {
+        // through shared memory, so that a store writes 64 bytes of each of eight rows, not 16 of 32
         tc_fence_after();
+        float* const buf = reinterpret_cast<float*>(gbase + C::kOut + t * C::kOutSlot + (warp & 3) * C::kOutWarp);
+        const uint32_t has = __ballot_sync(0xffffffffu, mine);
+        const size_t base_row = part + (static_cast<size_t>(it.row0) + it.q0) * a.Hq;
+        float* dst[4];  // of rows 8 i + lane / 4, this lane's four channels of sixteen
 #pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int q = rw + 8 * i + (lane >> 2), qt = q / a.g;
+          dst[i] = a.part_o + (base_row + static_cast<size_t>(tq * a.T + qt) * a.Hq + (q - qt * a.g)) * D + 4 * (lane & 3);
+        }
+#pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
           tmem_ld32(o_addr + 32 * c, o);
           tmem_wait_ld32(o);
-          if (mine) {
-            uint4* dst = reinterpret_cast<uint4*>(a.part_o + at * D + 32 * c);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) dst[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          for (int hf = 0; hf < 2; ++hf) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              *reinterpret_cast<uint4*>(buf + lane * kOutPitch + 4 * i) =
+                  make_uint4(o[16 * hf + 4 * i], o[16 * hf + 4 * i + 1], o[16 * hf + 4 * i + 2], o[16 * hf + 4 * i + 3]);
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint4 v = *reinterpret_cast<const uint4*>(buf + (8 * i + (lane >> 2)) * kOutPitch + 4 * (lane & 3));
+              if ((has >> (8 * i + (lane >> 2))) & 1u) *reinterpret_cast<uint4*>(dst[i] + 32 * c + 16 * hf) = v;
+            }
+            __syncwarp();
           }
         }
       }
@@ -1278,10 +1370,13 @@ Plan make_plan(const kvq_desc& d, int q_heads, int n_seqs, int n_rows, int max_r
   const long long by_rows = n_rows / tt + n_seqs, by_max = n_seqs * ((max_rows + tt - 1) / tt);
   p.tiles = p.few ? n_seqs : by_rows < by_max ? by_rows : by_max;
   // Few rows: eight CTAs an SM (four at a time), so that ragged sequences even out; 64 sequences of up
-  // to 8192 keys took 107 us with four an SM and 85 with eight, four of 32768 keys 43 and 45. Tiles: one
-  // CTA an SM, each with the query rows' set-up; 512 rows on 16384 keys took 222 us so and 269 with two.
+  // to 8192 keys took 107 us with four an SM and 85 with eight, four of 32768 keys 43 and 45. Tiles, each
+  // CTA with about 20000 clocks besides its keys: one CTA an SM at most where all sequences have the most
+  // rows (512 rows on 16384 keys took 212 us so, 269, 227 and 234 with three, four and six stretches),
+  // about two where they are ragged (twelve sequences of 1 to 131 rows on up to 8000 keys took 201 us with
+  // one stretch, 178 with two or three, 193 with six).
   const long long all = p.tiles * heads, keys = max_kv > 0 ? max_kv : 1;
-  long long n = all > 0 ? (p.few ? 8 : 1) * 148 / all : 1;
+  long long n = all <= 0 ? 1 : p.few ? 8 * 148 / all : by_rows < by_max ? (2 * 148 + all - 1) / all : 148 / all;
   const long long most = (keys + 511) / 512;  // of at least 512 keys
   n = n < 1 ? 1 : n > most ? most : n;
   if (n > 256) n = 256;
