@@ -17,10 +17,11 @@
 // k_paged_merge: a warp, or eight, per row and query head joins them with the sinks
 // and turns the result back.
 //
-// Measured, 32 / 8 heads of 128: 512 rows on 16384 keys of 4 bits 215 us = 650 TFLOP/s
-// (40 % of the products' rate): a slot's softmax of a tile, 2400 to 2800 clocks beside
-// the record warps, and its products take turns; tensor pipe 39 %, exponentials 40 %.
-// Twelve sequences of 1 to 131 rows on up to 8000 keys of 3 bits 205 us.
+// Measured, 32 / 8 heads of 128: 512 rows on 16384 keys of 4 bits 212 us = 660 TFLOP/s
+// (41 % of the products' rate): a slot's softmax of a tile, 2400 to 2800 clocks beside
+// the record warps, and its products take turns, 4370 clocks for two slots' tile; a CTA's
+// set-up, first tile and epilogue are 20000 more. Tensor pipe 39 %, exponentials 40 %.
+// Twelve sequences of 1 to 131 rows on up to 8000 keys of 3 bits 179 us.
 #include <math.h>
 
 #include "kvq_flash.cuh"

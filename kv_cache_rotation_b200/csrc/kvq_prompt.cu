@@ -15,9 +15,9 @@
 // Warps: 0-3 and 4-7 softmax of slots 0 and 1; 8 loads; 9 issues the products;
 // 10 and 11 clear what the mask hides in V (see below).
 //
-// Measured: 16384 tokens of 8 / 2 heads of 128, bf16, 521 us = 1055 TFLOP/s, at the
+// Measured: 16384 tokens of 8 / 2 heads of 128, bf16, 525 us = 1047 TFLOP/s, at the
 // power limit (1.37 GHz; tensor pipe and exponentials 51 % each, in turn). Nine
-// prompts, 6500 tokens, 32 / 8 heads, 122 us: set-up and epilogue of a CTA (about 5500
+// prompts, 6500 tokens, 32 / 8 heads, 118 us: set-up and epilogue of a CTA (about 4500
 // clocks) and a short grid's tail. One prompt of 77 tokens 8.5 us: a launch and one chain.
 //
 // Masked keys get weight 0, but 0 * inf is not 0, so V must be finite wherever
@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(Split<SLOTS>::kThreads, 3 - SLOTS)
   if (warp < LOAD) {
     more_regs<Split<SLOTS>::kSoftmax>();
     const int t = warp >> 2;
-    const int r = tid & 127, tok = q0 + t * a.T + r / a.g, j = r % a.g;
+    const int r = tid & 127, tok = q0 + t * a.T + r / a.g;
     const bool mine = r < a.T * a.g && tok < len;
     const int lim = mine ? tok + 1 : 0x7fffffff;  // a row of no token is computed unmasked and not stored
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(warp & 3) << 21);
@@ -150,7 +150,11 @@ __global__ void __launch_bounds__(Split<SLOTS>::kThreads, 3 - SLOTS)
       tc_fence_after();
       const float inv = st.l > 0.0f || st.l != st.l ? 1.0f / st.l : 0.0f;
       const bool dirty = *reinterpret_cast<volatile int*>(&m->dirty) != 0;
-      T* out = static_cast<T*>(a.p.out) + (static_cast<int64_t>(row0) + tok) * a.p.out_stride + (h * a.g + j) * D;
+      // Two slots (many CTAs): out over the slot's query rows, which nothing reads any more, so that a store writes
+      // 128 bytes of each of four rows and not 16 of 32 (nine prompts 118 us against 122). One slot (a call that does
+      // not fill the SMs): straight out, which is sooner done (77 tokens 8.5 us against 8.9).
+      uint8_t* const rows = gbase + t * C::kHead;
+      T* const own = static_cast<T*>(a.p.out) + (static_cast<int64_t>(row0) + tok) * a.p.out_stride + (h * a.g + r % a.g) * D;
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
         uint32_t o[32], w[16];
@@ -170,10 +174,27 @@ __global__ void __launch_bounds__(Split<SLOTS>::kThreads, 3 - SLOTS)
         }
 #pragma unroll
         for (int i = 0; i < 16; ++i) w[i] = Elem<T>::pack(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]));
-        if (mine) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            reinterpret_cast<uint4*>(out + 32 * c)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        for (int i = 0; i < 4; ++i) {
+          const uint4 four = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+          if constexpr (SLOTS == 2) *reinterpret_cast<uint4*>(rows + (c / 2) * kTileBytes + sw128(r, 4 * (c & 1) + i)) = four;
+          else if (mine) reinterpret_cast<uint4*>(own + 32 * c)[i] = four;
+        }
+      }
+      if constexpr (SLOTS == 2) {
+        __syncwarp();
+        int first = r & ~31;
+        asm volatile("" : "+r"(first));  // nothing of this is worked out before the loop and kept in registers
+#pragma unroll 2
+        for (int i = 0; i < 8; ++i) {
+          const int q = first + 4 * i + (lane >> 3), qt = q / a.g, at = q0 + t * a.T + qt;
+          if (qt >= a.T || at >= len) continue;
+          T* out = static_cast<T*>(a.p.out) + (static_cast<int64_t>(row0) + at) * a.p.out_stride +
+                   (h * a.g + q - qt * a.g) * D + 8 * (lane & 7);
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c)
+            *reinterpret_cast<uint4*>(out + 64 * c) =
+                *reinterpret_cast<const uint4*>(rows + c * kTileBytes + sw128(q, lane & 7));
         }
       }
     }
@@ -333,8 +354,8 @@ kvq_status run(const PromptArgs& p, cudaStream_t st, const LaunchCtx& ctx) {
 
 template <typename T, int D>
 kvq_status run_slots(const PromptArgs& p, cudaStream_t st, const LaunchCtx& ctx) {
-  // Two slots keep the tensor cores busier (nine prompts, 6500 tokens: 124 us against 132; 16384 tokens:
-  // 529 against 574); one slot is sooner done where the call does not fill the SMs (77 tokens: 8.5 us
+  // Two slots keep the tensor cores busier (nine prompts, 6500 tokens: 118 us against 132; 16384 tokens:
+  // 525 against 574); one slot is sooner done where the call does not fill the SMs (77 tokens: 8.5 us
   // against 10.3).
   return max_tiles(p, 2) * p.heads > ctx.num_sms ? run<T, D, 2>(p, st, ctx) : run<T, D, 1>(p, st, ctx);
 }
