@@ -21,7 +21,7 @@
 // (41 % of the products' rate): a slot's softmax of a tile, 2400 to 2800 clocks beside
 // the record warps, and its products take turns, 4370 clocks for two slots' tile; a CTA's
 // set-up, first tile and epilogue are 20000 more. Tensor pipe 39 %, exponentials 40 %.
-// Twelve sequences of 1 to 131 rows on up to 8000 keys of 3 bits 179 us.
+// Twelve sequences of 1 to 131 rows on up to 8000 keys of 3 bits 176 us.
 #include <math.h>
 
 #include "kvq_flash.cuh"
@@ -42,7 +42,8 @@ struct PagedArgs {
   int S, n_rows, max_pages, sink_rows, H, Hq, g, T, n_pages, n_sink, rope, rope_rows, rot, max_rows;
   int stretch, n_stretch, n_parts;  // keys of a CTA, CTAs along the keys, partial results per row
   int step_page, step_off;          // kFewStep keys in pages and a rest
-  FastDiv div_ps;
+  FastDiv div_ps, div_hq, div_g, div_stretch;  // page size, query heads, group, keys of a CTA
+  int part_per;                                // partial results of a stretch
   int64_t q_stride, out_stride;
   float scale, rscale;
   const __half* q;
@@ -688,17 +689,18 @@ __global__ void __launch_bounds__(256) k_paged_merge(const PagedArgs a) {
   __shared__ float nat[8][D];
   __shared__ float wtop[8], wsum[8];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, w = warp % W;
-  const long long wi = (blockIdx.x * 8ll + warp) / W;
-  const int row = static_cast<int>(wi / a.Hq), qh = static_cast<int>(wi % a.Hq);
+  // below 2^31 rows and query heads in all, and at most seven warps behind them
+  const uint32_t wi = W == 8 ? blockIdx.x : blockIdx.x * 8u + warp, wr = a.div_hq.div(wi);
+  const int row = static_cast<int>(wr), qh = static_cast<int>(a.div_hq.mod(wi, wr));
   // Every path waits for the tiles' grid: a kernel behind this one counts on both being done.
   auto after_tiles = [] { asm volatile("griddepcontrol.wait;" ::: "memory"); };
-  if (row >= a.n_rows) {  // the W warps of a row agree, here and below
+  if (wr >= static_cast<uint32_t>(a.n_rows)) {  // the W warps of a row agree, here and below
     after_tiles();
     return;
   }
   const int lo = seq_of_row(a.cu_rows, a.S, row, lane);
   const int b = min(max(__ldg(a.cu_rows + lo), 0), a.n_rows), e = min(max(__ldg(a.cu_rows + lo + 1), b), a.n_rows);
-  const int h = qh / a.g, len = max(__ldg(a.kv_len + lo), 0);
+  const int h = static_cast<int>(a.div_g.div(static_cast<uint32_t>(qh))), len = max(__ldg(a.kv_len + lo), 0);
   if (row < b || row >= e || row - b >= a.max_rows) {
     after_tiles();
     return;
@@ -758,13 +760,21 @@ __global__ void __launch_bounds__(256) k_paged_merge(const PagedArgs a) {
   after_tiles();
   // the stretches that hold keys of this row, an empty part (weight total 0) left out
   const size_t rows = static_cast<size_t>(a.n_rows) * a.Hq, me = static_cast<size_t>(row) * a.Hq + qh;
-  const int per = a.n_parts / a.n_stretch;
-  const int parts = lim > 0 ? min(a.n_stretch, (lim - 1) / a.stretch + 1) * per : 0;
+  const int reach = static_cast<int>(a.div_stretch.div(static_cast<uint32_t>(max(lim, 1) - 1)));  // the stretch of the last key
+  const int parts = lim > 0 ? min(a.n_stretch, reach + 1) * a.part_per : 0;
   auto part = [&](int p) { return p < parts ? a.part_s[p * rows + me] : make_float2(-INFINITY, 0.0f); };
   float all_top = top;
-  for (int p0 = w; p0 < parts; p0 += 32 * W) {
-    const float2 s = part(p0 + lane * W);
-    all_top = fmaxf(all_top, all_max(s.y != 0.0f ? s.x : -INFINITY));
+  if constexpr (W == 1) {  // at most kNarrow parts: every lane reads the statistics
+#pragma unroll 2
+    for (int p = 0; p < parts; ++p) {
+      const float2 s = part(p);
+      all_top = fmaxf(all_top, s.y != 0.0f ? s.x : -INFINITY);
+    }
+  } else {
+    for (int p0 = w; p0 < parts; p0 += 32 * W) {
+      const float2 s = part(p0 + lane * W);
+      all_top = fmaxf(all_top, all_max(s.y != 0.0f ? s.x : -INFINITY));
+    }
   }
   if constexpr (W > 1) {
     if (lane == 0) wtop[warp] = all_top;
@@ -778,7 +788,18 @@ __global__ void __launch_bounds__(256) k_paged_merge(const PagedArgs a) {
 #pragma unroll
   for (int c = 0; c < C; ++c) o[c] = 0.0f, own[c] *= fs;
   total *= fs;
-  for (int p0 = w; p0 < parts; p0 += 32 * W) {
+  if constexpr (W == 1) {
+#pragma unroll 2
+    for (int p = 0; p < parts; ++p) {
+      const float2 s = part(p);
+      if (s.y == 0.0f) continue;  // what an empty part's sums hold is not read
+      const float f = exp2f(s.x - ref);
+      const float* src = a.part_o + (p * rows + me) * D;
+      total = fmaf(s.y, f, total);
+#pragma unroll
+      for (int c = 0; c < C; ++c) o[c] = fmaf(src[TILE ? tile_pos<BITS>(lane * C + c) : lane * C + c], f, o[c]);
+    }
+  } else for (int p0 = w; p0 < parts; p0 += 32 * W) {
     const float2 s = part(p0 + lane * W);
     const bool live = s.y != 0.0f;
     const float f = live ? exp2f(s.x - ref) : 0.0f;
@@ -1407,10 +1428,11 @@ kvq_status run_few(const PagedArgs& a, long long grid, cudaStream_t st) {
   return launch_status();
 }
 
-// Eight warps a row where there are more parts than one warp reads in one go.
+// Eight warps a row where there are more parts than a warp should read one after the other.
+constexpr int kNarrow = 8;
 template <int D, int BITS, bool TILE>
 kvq_status run_merge(const PagedArgs& a, cudaStream_t st) {
-  const bool wide = a.n_parts > 8;
+  const bool wide = a.n_parts > kNarrow;
   cudaLaunchConfig_t cfg{};
   const long long warps = static_cast<long long>(a.n_rows) * a.Hq * (wide ? 8 : 1);
   cfg.gridDim = dim3(static_cast<unsigned>((warps + 7) / 8));
@@ -1479,6 +1501,10 @@ kvq_status launch_attend_paged(const kvq_desc& dk, const kvq_desc&, const void* 
   a.n_stretch = p.n_stretch;
   a.n_parts = p.n_parts;
   a.div_ps = FastDiv(static_cast<uint32_t>(dk.t_cap));
+  a.div_hq = FastDiv(static_cast<uint32_t>(q_heads));
+  a.div_g = FastDiv(static_cast<uint32_t>(a.g));
+  a.div_stretch = FastDiv(static_cast<uint32_t>(p.stretch));
+  a.part_per = p.n_parts / p.n_stretch;
   a.step_page = kFewStep / dk.t_cap;
   a.step_off = kFewStep % dk.t_cap;
   a.q_stride = q_stride;
