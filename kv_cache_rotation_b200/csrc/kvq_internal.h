@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <mutex>
+
 #include "kvq.h"
 
 namespace kvq {
@@ -101,10 +103,12 @@ struct PromptArgs {
 };
 kvq_status launch_attend_prompt(const PromptArgs& p, cudaStream_t st, const LaunchCtx& ctx);
 
-// cudaFuncSetAttribute(MaxDynamicSharedMemorySize) only when a kernel needs
-// more dynamic shared memory on this device than it was last granted (the
-// attribute persists per device). A small per-thread cache of (kernel,
-// device, bytes) keeps the host cost of repeated launches low.
+// Let a kernel use up to `bytes` of dynamic shared memory on the current device. Without leave a block has
+// 48 KB, its static arrays included. The attribute belongs to the function on the device, not to the thread
+// that sets it, so it is read and set under one lock and only ever raised: a thread whose call needs less
+// never takes away what another thread counts on. A small cache per thread of (kernel, device, bytes
+// granted) keeps the host cost of repeated launches low.
+inline std::mutex g_smem_mu;
 inline bool set_smem_once(const void* fn, size_t bytes) {
   struct Entry {
     const void* fn;
@@ -117,9 +121,20 @@ inline bool set_smem_once(const void* fn, size_t bytes) {
   if (cudaGetDevice(&dev) != cudaSuccess) return false;
   for (int i = 0; i < n; ++i)
     if (cache[i].fn == fn && cache[i].dev == dev && bytes <= cache[i].bytes) return true;
-  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)) !=
-      cudaSuccess)
-    return false;
+  {
+    std::lock_guard<std::mutex> lk(g_smem_mu);
+    cudaFuncAttributes now;
+    if (cudaFuncGetAttributes(&now, fn) != cudaSuccess) return false;
+    constexpr size_t kNoLeave = 48 * 1024;
+    const size_t set = static_cast<size_t>(now.maxDynamicSharedSizeBytes);
+    if (bytes + now.sharedSizeBytes > kNoLeave) {
+      const size_t want = bytes > set ? bytes : set;
+      if ((set < bytes || set <= kNoLeave) &&
+          cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(want)) != cudaSuccess)
+        return false;
+      bytes = want;
+    }
+  }
   for (int i = 0; i < n; ++i)
     if (cache[i].fn == fn && cache[i].dev == dev) {
       cache[i].bytes = bytes;

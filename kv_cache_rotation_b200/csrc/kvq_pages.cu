@@ -590,8 +590,10 @@ kvq_status launch_page_map(const kvq_desc& d, const kvq_paged& pg, const int32_t
   a.pos = pg.pos;
   a.slot = pg.slot;
   a.report = report;
+  // Allowed for on every call, also below 48 KB: that limit covers the kernel's static arrays too, so 6096
+  // sequences (48776 bytes, and 384 static) are above it.
   const size_t smem = 2 * (static_cast<size_t>(pg.n_seqs) + 1) * 4;
-  if (smem > 48 * 1024 && !set_smem_once(reinterpret_cast<const void*>(k_page_map), smem)) return KVQ_ERR_CUDA;
+  if (!set_smem_once(reinterpret_cast<const void*>(k_page_map), smem)) return KVQ_ERR_CUDA;
   long long grid = (static_cast<long long>(pg.n_rows) + 4 * kMapThreads - 1) / (4 * kMapThreads);
   if (grid > ctx.num_sms) grid = ctx.num_sms;
   if (grid < 1) grid = 1;
