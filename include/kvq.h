@@ -280,7 +280,9 @@ size_t kvq_attend_workspace_bytes(const kvq_desc* dk, const kvq_desc* dv, int32_
  * The rows of a call (new tokens) are packed on one axis: sequence s has the rows
  * cu_rows[s] .. cu_rows[s+1]-1, in token order. All pointers are device pointers, int32; kvq_page_map
  * fills them, or the caller does. Values that do not fit (a slot outside the pool, a page outside
- * 0..batch-1, a position without a RoPE row) are never followed: the row or the key is left out. */
+ * 0..batch-1, a position without a RoPE row) are never followed: the row or the key is left out.
+ * Encode, decode and attention without rows (n_rows = 0, a step in which no sequence has a new token)
+ * do nothing and return KVQ_OK; the arrays and tensors of rows may be NULL then, as empty ones are. */
 typedef struct {
   int32_t n_seqs;       /* S >= 0 sequences */
   int32_t n_rows;       /* rows of the packed axis; rows behind cu_rows[S] belong to no sequence */
@@ -367,7 +369,7 @@ enum { KVQ_F16 = 0, KVQ_BF16 = 1 };
  *   scale    finite, > 0
  * Scores, statistics and sums are held in fp32, the weights enter the product with v rounded to
  * `dtype`. What lies outside a row's view (later rows, other sequences, rows of no sequence) has no
- * effect on it, infinities and NaN included. */
+ * effect on it, infinities and NaN included. q, k, v and out may be NULL when n_rows = 0. */
 kvq_status kvq_attend_prompt(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
                              int64_t v_stride, int32_t n_seqs, int32_t n_rows, int32_t q_heads, int32_t heads,
                              int32_t head_dim, int32_t dtype, const int32_t* cu_rows, int32_t max_rows, float scale,

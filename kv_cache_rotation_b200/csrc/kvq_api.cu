@@ -438,12 +438,13 @@ kvq_status check_paged(const kvq_desc& d, const kvq_paged* pg) {
   return KVQ_OK;
 }
 
-// Row maps of encode / decode, and the tables without a sink list.
+// Row maps of encode / decode, and the tables without a sink list. A step without rows has empty tensors,
+// whose addresses may be null, here and in the attention calls.
 kvq_status check_rows(const kvq_desc& d, const kvq_paged& pg, const kvq_tables* tb, const kvq_packed* c,
                       int64_t stride) {
   if (!tb) return KVQ_ERR_INVALID;
   if (d.n_sink > 0 && tb->sink_pos) return KVQ_ERR_UNSUPPORTED;
-  if (!pg.pos || !pg.slot || (d.n_sink > 0 && !pg.seq)) return KVQ_ERR_INVALID;
+  if (pg.n_rows > 0 && (!pg.pos || !pg.slot || (d.n_sink > 0 && !pg.seq))) return KVQ_ERR_INVALID;
   if (!aligned(pg.pos, 16) || !aligned(pg.slot, 16) || (pg.seq && !aligned(pg.seq, 16)) ||
       (pg.sink_slot && !aligned(pg.sink_slot, 4)))
     return KVQ_ERR_ALIGN;
@@ -482,7 +483,7 @@ kvq_status kvq_encode_paged(const kvq_desc* d, const void* x, int64_t x_stride, 
   kvq_desc p;
   kvq_status s = check_paged_desc(d, &p);
   if (s != KVQ_OK || (s = check_paged(p, pg)) != KVQ_OK) return s;
-  if (!x) return KVQ_ERR_INVALID;
+  if (!x && pg->n_rows > 0) return KVQ_ERR_INVALID;
   if (!aligned(x, 16)) return KVQ_ERR_ALIGN;
   if ((s = check_rows(p, *pg, tb, out, x_stride)) != KVQ_OK) return s;
   if (pg->n_rows == 0) return KVQ_OK;
@@ -496,7 +497,7 @@ kvq_status kvq_decode_paged(const kvq_desc* d, const kvq_packed* in, const kvq_p
   kvq_desc p;
   kvq_status s = check_paged_desc(d, &p);
   if (s != KVQ_OK || (s = check_paged(p, pg)) != KVQ_OK) return s;
-  if (!x_out || (out_fp32 != 0 && out_fp32 != 1)) return KVQ_ERR_INVALID;
+  if ((!x_out && pg->n_rows > 0) || (out_fp32 != 0 && out_fp32 != 1)) return KVQ_ERR_INVALID;
   if (!aligned(x_out, 16)) return KVQ_ERR_ALIGN;
   if ((s = check_rows(p, *pg, tb, in, x_stride)) != KVQ_OK) return s;
   if (pg->n_rows == 0) return KVQ_OK;
@@ -541,7 +542,7 @@ kvq_status kvq_attend_paged(const kvq_desc* dk, const kvq_desc* dv, const void* 
   kvq_desc k, v;
   kvq_status s = check_attend_paged(dk, dv, q_heads, pg, max_rows, max_kv, &k, &v);
   if (s != KVQ_OK) return s;
-  if (!q || !out || !workspace || !good_scale(scale)) return KVQ_ERR_INVALID;
+  if (((!q || !out) && pg->n_rows > 0) || !workspace || !good_scale(scale)) return KVQ_ERR_INVALID;
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(workspace, 256)) return KVQ_ERR_ALIGN;
   if (q_stride < static_cast<int64_t>(q_heads) * k.head_dim || out_stride < static_cast<int64_t>(q_heads) * k.head_dim)
     return KVQ_ERR_INVALID;
@@ -572,7 +573,7 @@ kvq_status kvq_attend_prompt(const void* q, int64_t q_stride, const void* k, int
   if (q_heads / heads > 128 || heads > 65535) return KVQ_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(n_rows) * q_heads >= (int64_t(1) << 31)) return KVQ_ERR_UNSUPPORTED;
   if (!good_scale(scale)) return KVQ_ERR_INVALID;
-  if (!q || !k || !v || !out || !cu_rows) return KVQ_ERR_INVALID;
+  if (((!q || !k || !v || !out) && n_rows > 0) || !cu_rows) return KVQ_ERR_INVALID;
   if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) || !aligned(cu_rows, 4))
     return KVQ_ERR_ALIGN;
   const int64_t qw = static_cast<int64_t>(q_heads) * head_dim, kw = static_cast<int64_t>(heads) * head_dim;

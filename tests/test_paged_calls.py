@@ -90,3 +90,60 @@ def test_page_map_of_two_threads_with_different_sizes():
     torch.cuda.synchronize()
     check_big()
     assert K.kvq_check(0) == K.KVQ_OK
+
+
+# ---------------------------------------------------------------- steps without rows
+def test_calls_without_rows_take_null_tensors():
+    """An empty tensor's address is null."""
+    d = TA.make_desc(batch=16, heads=2, head_dim=128, tokens=0, t_cap=32, bits=2)
+    pg = K.kvq_paged()
+    pg.n_seqs, pg.n_rows, pg.max_pages = 2, 0, 4
+    pg.cu_rows = pg.kv_len = pg.block_table = 4096
+    pk, tb = K.kvq_packed(), K.kvq_tables()
+    pk.codes = pk.scale_zero = 4096
+    assert K.kvq_encode_paged(d, None, 256, pg, tb, pk) == K.KVQ_OK
+    assert K.kvq_decode_paged(d, pk, pg, tb, None, 256, 0) == K.KVQ_OK
+    n = K.kvq_attend_paged_workspace_bytes(d, d, 8, pg, 0, 100)
+    assert n > 0
+    assert K.kvq_attend_paged(d, d, None, 1024, 8, pk, tb, pk, tb, pg, 0, 100, 0.1, None, 1024, 4096, n) == K.KVQ_OK
+    assert K.kvq_attend_prompt(None, 1024, None, 256, None, 256, 2, 0, 8, 2, 128, 0, 4096, 0, 0.1, None, 1024) == K.KVQ_OK
+    pg.n_rows = 1  # with a row they are refused as ever
+    assert K.kvq_encode_paged(d, None, 256, pg, tb, pk) == K.KVQ_ERR_INVALID
+    assert K.kvq_encode_paged(d, 4096, 256, pg, tb, pk) == K.KVQ_ERR_INVALID
+    assert K.kvq_decode_paged(d, pk, pg, tb, None, 256, 0) == K.KVQ_ERR_INVALID
+    assert K.kvq_attend_paged(d, d, None, 1024, 8, pk, tb, pk, tb, pg, 1, 100, 0.1, None, 1024, 4096, 1 << 30) == K.KVQ_ERR_INVALID
+    assert K.kvq_attend_prompt(None, 1024, None, 256, None, 256, 2, 1, 8, 2, 128, 0, 4096, 1, 0.1, None, 1024) == K.KVQ_ERR_INVALID
+
+
+@gpu
+@pytest.mark.parametrize("n_sink", [0, 4])
+def test_a_step_in_which_no_sequence_has_a_new_token(n_sink):
+    Hq, H, D, ps, S = 8, 2, 128, 16, 3
+    common = dict(batch=12, heads=H, head_dim=D, tokens=0, t_cap=ps, bits=2, n_sink=n_sink)
+    dk, dv = TA.make_desc(rope=1, **common), TA.make_desc(rope=0, **common)
+    tk, tv = TA.make_tables(rope_cs=TA.rope_table(64, D)), TA.make_tables()
+    kc, vc = TA.alloc_paged(dk, S), TA.alloc_paged(dv, S)
+    table = torch.full((S, 4), -1, dtype=torch.int32, device="cuda")
+    free, used, ctx = _i32(list(range(12))), _i32([0]), _i32([0] * S)
+    for new in ([20, 3, 0], [0, 0, 0], [1, 0, 2], [0, 0, 0]):
+        n = sum(new)
+        b = TA.make_paged(S, n, 4, block_table=table)
+        before, codes = table.clone(), kc.codes.clone()
+        rep = TA.page_map(dk, b, ctx, _i32(new), free, used)
+        x = torch.randn(n, Hq + 2 * H, D, device="cuda").half()
+        TA.encode_paged(dk, x[:, Hq:Hq + H], b, tk, kc)
+        TA.encode_paged(dv, x[:, Hq + H:], b, tv, vc)
+        back = torch.empty(n, H, D, dtype=torch.float16, device="cuda")
+        TA.decode_paged(dk, kc, b, tk, back)
+        out = torch.empty(n, Hq, D, dtype=torch.float16, device="cuda")
+        ws = TA.attend_paged_workspace(dk, dv, Hq, b, max(new), 64)
+        TA.attend_paged(dk, dv, x[:, :Hq], kc, tk, vc, tv, b, max(new), 64, D ** -0.5, out, ws)
+        empty = TA.attend_prompt(x[:, :Hq], x[:, Hq:Hq + H], x[:, Hq + H:], b.cu_rows, max(new), 0.1)
+        assert K.kvq_check(0) == K.KVQ_OK and empty.shape == out.shape
+        assert rep.tolist()[0] == n and rep.tolist()[2:] == [0, 0]
+        assert b.kv_len.tolist() == (ctx + _i32(new)).tolist()
+        if n == 0:
+            assert torch.equal(table, before) and torch.equal(kc.codes, codes)
+        else:
+            assert torch.isfinite(out).all() and torch.isfinite(back).all()
+        ctx, used = b.kv_len, rep[1:2].clone()
