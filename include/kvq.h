@@ -305,7 +305,9 @@ typedef struct {
  * for every row seq, pos and slot (-1 in rows that belong to no sequence).
  * report int32[4]: rows of all sequences; free pages taken in all, earlier calls' included (the next
  * call's free_used); rows without a slot because the pool or a block_table row ran out (their pages
- * read -1); pages that were lacking. report must not overlap free_used.
+ * read -1); pages that were lacking.
+ * No array that is written may overlap another one of the call (KVQ_ERR_INVALID): blocks read the lengths
+ * while others write, so the next step's ctx_len is a copy of kv_len, and its free_used one of report[1].
  * Of pg n_seqs, n_rows, max_pages and the six arrays are used; of d batch and t_cap. n_seqs <= 16384
  * (else KVQ_ERR_UNSUPPORTED). One launch; the result does not depend on scheduling. */
 kvq_status kvq_page_map(const kvq_desc* d, const kvq_paged* pg, const int32_t* ctx_len, const int32_t* new_len,

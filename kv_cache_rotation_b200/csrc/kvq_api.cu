@@ -467,11 +467,24 @@ kvq_status kvq_page_map(const kvq_desc* d, const kvq_paged* pg, const int32_t* c
   if (n_free < 0 || (n_free > 0 && !free_pages) || !free_used || !report) return KVQ_ERR_INVALID;
   if (pg->n_seqs > 0 && (!ctx_len || !new_len || !pg->kv_len || !pg->block_table)) return KVQ_ERR_INVALID;
   if (!pg->cu_rows || (pg->n_rows > 0 && (!pg->seq || !pg->pos || !pg->slot))) return KVQ_ERR_INVALID;
-  if (report == free_used) return KVQ_ERR_INVALID;
   if (!aligned(pg->seq, 16) || !aligned(pg->pos, 16) || !aligned(pg->slot, 16) || !aligned(pg->cu_rows, 4) ||
       !aligned(pg->kv_len, 4) || !aligned(pg->block_table, 4) || !aligned(ctx_len, 4) || !aligned(new_len, 4) ||
       !aligned(free_pages, 4) || !aligned(free_used, 4) || !aligned(report, 4))
     return KVQ_ERR_ALIGN;
+  // what is written (the first seven) apart from everything else
+  const int64_t S = pg->n_seqs, n = pg->n_rows;
+  const struct {
+    const int32_t* p;
+    int64_t n;
+  } arrays[] = {{pg->cu_rows, S + 1}, {pg->kv_len, S}, {pg->block_table, S * pg->max_pages}, {pg->seq, n},
+                {pg->pos, n},         {pg->slot, n},   {report, 4},                          {ctx_len, S},
+                {new_len, S},         {free_pages, n_free}, {free_used, 1}};
+  for (int i = 0; i < 7; ++i)
+    for (int j = i + 1; j < 11; ++j) {
+      const uintptr_t a = reinterpret_cast<uintptr_t>(arrays[i].p), b = reinterpret_cast<uintptr_t>(arrays[j].p);
+      if (arrays[i].n > 0 && arrays[j].n > 0 && a < b + 4 * arrays[j].n && b < a + 4 * arrays[i].n)
+        return KVQ_ERR_INVALID;
+    }
   LaunchCtx ctx;
   if ((s = get_ctx(&ctx)) != KVQ_OK) return s;
   return launch_page_map(p, *pg, ctx_len, new_len, free_pages, n_free, free_used, report,

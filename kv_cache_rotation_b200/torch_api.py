@@ -442,6 +442,12 @@ def _here(*tensors) -> None:
             raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{dev}")
 
 
+def _meet(a: torch.Tensor, b: torch.Tensor) -> bool:
+    """Whether two contiguous tensors share memory."""
+    return (a.numel() > 0 and b.numel() > 0 and a.data_ptr() < b.data_ptr() + b.numel() * b.element_size()
+            and b.data_ptr() < a.data_ptr() + a.numel() * a.element_size())
+
+
 def _rows(t: torch.Tensor, name: str, dtypes, heads=None, dim=None) -> int:
     """Elements between the packed rows of t [n_rows][heads][dim]; the rows themselves are dense."""
     if not isinstance(t, torch.Tensor):
@@ -490,8 +496,13 @@ def bind_page_map(d: kvq_desc, batch: Paged, ctx_len: torch.Tensor, new_len: tor
     _req(free_pages, "free_pages", (torch.int32,), (free_pages.numel(),))
     _req(free_used, "free_used", (torch.int32,), (1,))
     _req(report, "report", (torch.int32,), (4,))
-    if report.data_ptr() <= free_used.data_ptr() < report.data_ptr() + 16:
-        raise ValueError("report: must not overlap free_used")
+    reads = dict(ctx_len=ctx_len, new_len=new_len, free_pages=free_pages, free_used=free_used)
+    writes = {n: getattr(batch, n) for n in ("cu_rows", "kv_len", "block_table", "seq", "pos", "slot")}
+    writes["report"] = report
+    for i, (name, t) in enumerate(writes.items()):
+        for other, u in [*list(writes.items())[i + 1:], *reads.items()]:
+            if _meet(t, u):
+                raise ValueError(f"{name}: written while {other} is read or written, they must not overlap")
     _here(batch.cu_rows, batch.block_table, batch.seq, ctx_len, new_len, free_pages, free_used, report)
     args = (ctypes.byref(d), ctypes.byref(p), ctx_len.data_ptr(), new_len.data_ptr(), free_pages.data_ptr(),
             free_pages.numel(), free_used.data_ptr(), report.data_ptr())
@@ -501,7 +512,8 @@ def bind_page_map(d: kvq_desc, batch: Paged, ctx_len: torch.Tensor, new_len: tor
 def page_map(d: kvq_desc, batch: Paged, ctx_len: torch.Tensor, new_len: torch.Tensor, free_pages: torch.Tensor,
              free_used: torch.Tensor, report: torch.Tensor = None, stream=None) -> torch.Tensor:
     """Fill the batch from its lengths (kvq_page_map); returns the report, int32 [4]: rows, free pages
-    taken in all, rows without a slot, pages that were lacking. report[1:2] is the next call's free_used."""
+    taken in all, rows without a slot, pages that were lacking. report[1:2] is the next call's free_used, and
+    batch.kv_len its ctx_len: copies of them where the next call writes the same tensors."""
     if report is None:
         report = torch.empty(4, dtype=torch.int32, device=ctx_len.device)
     bind_page_map(d, batch, ctx_len, new_len, free_pages, free_used, report, stream)()

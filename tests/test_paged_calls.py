@@ -147,3 +147,48 @@ def test_a_step_in_which_no_sequence_has_a_new_token(n_sink):
         else:
             assert torch.isfinite(out).all() and torch.isfinite(back).all()
         ctx, used = b.kv_len, rep[1:2].clone()
+
+
+# ---------------------------------------------------------------- arrays that overlap
+MAP = dict(cu_rows=3, kv_len=2, block_table=8, seq=8, pos=8, slot=8, report=4, ctx_len=2, new_len=2, free_pages=9, free_used=1)
+WRITTEN = list(MAP)[:7]
+
+
+@pytest.mark.parametrize("one,other", [(a, b) for i, a in enumerate(WRITTEN) for b in list(MAP)[i + 1:]])
+def test_page_map_refuses_arrays_that_overlap(one, other):
+    """Blocks read lengths while others write: kv_len as the next step's ctx_len would race. Addresses that
+    nothing follows: without a device a call that is not refused ends there."""
+    if torch.cuda.is_available():
+        pytest.skip("made-up addresses")
+    at = {n: 1 << 20 | i << 12 for i, n in enumerate(MAP)}
+
+    def call():
+        pg = K.kvq_paged()
+        pg.n_seqs, pg.n_rows, pg.max_pages = 2, 8, 4
+        for n in ("cu_rows", "kv_len", "block_table", "seq", "pos", "slot"):
+            setattr(pg, n, at[n])
+        d = TA.make_desc(batch=16, heads=1, tokens=0, t_cap=16, bits=2)
+        return K.kvq_page_map(d, pg, at["ctx_len"], at["new_len"], at["free_pages"], 9, at["free_used"], at["report"])
+    assert call() == K.KVQ_ERR_CUDA
+    last = at[one] + 4 * (MAP[one] - 1)
+    if other in ("seq", "pos", "slot"):  # on their own alignment
+        last &= ~15
+    at[other] = last  # its first word on the other's last
+    assert call() == K.KVQ_ERR_INVALID
+
+
+@gpu
+def test_page_map_binding_refuses_its_own_lengths_and_takes_copies():
+    d = TA.make_desc(batch=8, heads=1, tokens=0, t_cap=16, bits=2)
+    b = TA.make_paged(2, 3, 4)
+    free, new, report = _i32(list(range(8))), _i32([2, 1]), torch.zeros(4, dtype=torch.int32, device="cuda")
+    TA.page_map(d, b, _i32([0, 0]), new, free, _i32([0]), report)
+    with pytest.raises(ValueError, match="kv_len"):
+        TA.page_map(d, b, b.kv_len, new, free, _i32([2]))
+    with pytest.raises(ValueError, match="report"):
+        TA.page_map(d, b, _i32([2, 1]), new, free, report[1:2], report)
+    with pytest.raises(ValueError, match="seq"):
+        TA.page_map(d, TA.Paged(b.cu_rows, b.kv_len, b.block_table, b.seq, b.seq, b.slot), _i32([2, 1]), new, free, _i32([2]))
+    for _ in range(3):  # one batch for all steps
+        rep = TA.page_map(d, b, b.kv_len.clone(), new, free, report[1:2].clone(), report)
+    assert b.kv_len.tolist() == [8, 4] and rep.tolist() == [3, 2, 0, 0] and b.pos.tolist() == [6, 7, 3]
