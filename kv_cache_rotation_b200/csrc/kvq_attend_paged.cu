@@ -1336,7 +1336,9 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 4 : 2) k_paged_few(cons
   const size_t part = static_cast<size_t>(z * kFewWarps + warp) * (static_cast<size_t>(a.n_rows) * a.Hq);
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
-    if (bad < lim[t]) lr[t] = NAN;
+    // an infinite reference (a value scale that is infinite, on a key all rows see) leaves every weight zero, and
+    // a part without weights would pass for an empty one
+    if (bad < lim[t] || mr[t] == INFINITY) lr[t] = NAN;
 #pragma unroll
     for (int o = 4; o < 32; o <<= 1) {
       lr[t] += __shfl_xor_sync(0xffffffffu, lr[t], o);

@@ -192,3 +192,25 @@ def test_page_map_binding_refuses_its_own_lengths_and_takes_copies():
     for _ in range(3):  # one batch for all steps
         rep = TA.page_map(d, b, b.kv_len.clone(), new, free, report[1:2].clone(), report)
     assert b.kv_len.tolist() == [8, 4] and rep.tolist() == [3, 2, 0, 0] and b.pos.tolist() == [6, 7, 3]
+
+
+# ---------------------------------------------------------------- records that are not finite
+@gpu
+@pytest.mark.parametrize("S,Z", [(0x7c00, 0x3c00), (0xfc00, 0x3c00), (0x3c00, 0xfc00), (0x3c00, 0x7c00), (0x7e00, 0x7e00)],
+                         ids=["scale inf", "scale -inf", "zero -inf", "zero inf", "nan"])
+@pytest.mark.parametrize("new,Hq,bits,group,ctx", [
+    ([1, 1], 4, 2, 128, 100), ([1, 1], 8, 4, 64, 1500), ([2, 1], 4, 2, 32, 100),  # few rows: one column tile, two
+    ([20, 1], 8, 3, 32, 100), ([200, 3], 8, 4, 64, 600)])                         # one slot of rows, two
+def test_a_cached_value_that_is_not_finite_shows_in_every_row_that_sees_it(new, Hq, bits, group, ctx, S, Z):
+    """sum_n p_n v_n has no finite value then; it must not pass as the sum over the other keys."""
+    from test_paged import Attend
+    t = Attend([ctx, ctx], new, Hq, 2, 128, bits, group, 0, False, 0, "fwht_head", 16, extra=1)
+    t.call()()
+    clean = t.out.clone()
+    sz = t.packs[1].scale_zero
+    sz[t.b.m["block_table"][0][37 // 16], :, 37 % 16] = torch.tensor([S, Z], dtype=torch.int32).to(torch.int16).cuda()
+    t.out.fill_(7.0)
+    t.call()()
+    assert K.kvq_check(0) == K.KVQ_OK
+    assert not torch.isfinite(t.out[:new[0]]).all(-1).any()
+    assert torch.equal(t.out[new[0]:], clean[new[0]:])
