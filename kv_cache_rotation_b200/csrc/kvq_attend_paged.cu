@@ -1240,12 +1240,21 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 4 : 2) k_paged_few(cons
     float lga, lgb;
     asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(lga) : "f"(ta));
     asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(lgb) : "f"(tb));
+    // 0, or NaN where a key's scale or zero is not finite: its channels are infinities of both signs or NaN then,
+    // and S sum q'c + Z sum q' alone could be -infinity, which would hide the key
+    float offa = 0.0f, offb = 0.0f;
+#pragma unroll
+    for (int k = 0; k < NG; ++k) {
+      const float2 za = h2f2(ka[k]), zb = h2f2(kb2[k]);
+      offa = fmaf(za.x + za.y, 0.0f, offa);
+      offb = fmaf(zb.x + zb.y, 0.0f, offb);
+    }
     uint32_t wa2[NT][NG], wb2[NT][NG];
     float sa[NT], sb[NT];
     bool raise = false;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      sa[t] = sb[t] = 0.0f;
+      sa[t] = offa, sb[t] = offb;
 #pragma unroll
       for (int k = 0; k < NG; ++k) {
         const float2 za = h2f2(ka[k]), zb = h2f2(kb2[k]);

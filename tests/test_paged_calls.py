@@ -201,13 +201,15 @@ def test_page_map_binding_refuses_its_own_lengths_and_takes_copies():
 @pytest.mark.parametrize("new,Hq,bits,group,ctx", [
     ([1, 1], 4, 2, 128, 100), ([1, 1], 8, 4, 64, 1500), ([2, 1], 4, 2, 32, 100),  # few rows: one column tile, two
     ([20, 1], 8, 3, 32, 100), ([200, 3], 8, 4, 64, 600)])                         # one slot of rows, two
-def test_a_cached_value_that_is_not_finite_shows_in_every_row_that_sees_it(new, Hq, bits, group, ctx, S, Z):
-    """sum_n p_n v_n has no finite value then; it must not pass as the sum over the other keys."""
+@pytest.mark.parametrize("which", [1, 0], ids=["value", "key"])
+def test_a_cached_record_that_is_not_finite_shows_in_every_row_that_sees_it(which, new, Hq, bits, group, ctx, S, Z):
+    """sum_n p_n v_n has no finite value then; it must not pass as the sum over the other keys. A key's channels are
+    infinities of both signs (or NaN), and so is its score."""
     from test_paged import Attend
     t = Attend([ctx, ctx], new, Hq, 2, 128, bits, group, 0, False, 0, "fwht_head", 16, extra=1)
     t.call()()
     clean = t.out.clone()
-    sz = t.packs[1].scale_zero
+    sz = t.packs[which].scale_zero
     sz[t.b.m["block_table"][0][37 // 16], :, 37 % 16] = torch.tensor([S, Z], dtype=torch.int32).to(torch.int16).cuda()
     t.out.fill_(7.0)
     t.call()()
