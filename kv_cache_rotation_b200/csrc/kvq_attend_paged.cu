@@ -1157,10 +1157,13 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 4 : 2) k_paged_few(cons
     lim[t] = r < n_rows ? pos0 + r / a.g + 1 : 0x7fffffff;
   }
 
-  float acc[8][NT][4], mr[NT], lr[NT], zr[NT][NG];
+  // low: the lowest score of the keys that the row sees. A key whose scale or zero is not finite has channels of
+  // both infinities, or NaN, and no score; S sum q'c + Z sum q' alone could be -infinity, which would hide the key.
+  float acc[8][NT][4], mr[NT], lr[NT], zr[NT][NG], low[NT];
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     mr[t] = -INFINITY;
+    low[t] = INFINITY;
     lr[t] = 0.0f;
 #pragma unroll
     for (int k = 0; k < NG; ++k) zr[t][k] = 0.0f;
@@ -1240,31 +1243,24 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 4 : 2) k_paged_few(cons
     float lga, lgb;
     asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(lga) : "f"(ta));
     asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(lgb) : "f"(tb));
-    // 0, or NaN where a key's scale or zero is not finite: its channels are infinities of both signs or NaN then,
-    // and S sum q'c + Z sum q' alone could be -infinity, which would hide the key
-    float offa = 0.0f, offb = 0.0f;
-#pragma unroll
-    for (int k = 0; k < NG; ++k) {
-      const float2 za = h2f2(ka[k]), zb = h2f2(kb2[k]);
-      offa = fmaf(za.x + za.y, 0.0f, offa);
-      offb = fmaf(zb.x + zb.y, 0.0f, offb);
-    }
     uint32_t wa2[NT][NG], wb2[NT][NG];
     float sa[NT], sb[NT];
     bool raise = false;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      sa[t] = offa, sb[t] = offb;
+      sa[t] = sb[t] = 0.0f;
 #pragma unroll
       for (int k = 0; k < NG; ++k) {
         const float2 za = h2f2(ka[k]), zb = h2f2(kb2[k]);
         sa[t] = fmaf(za.x * mul[t], sc[k][t][0] + sc[k][t][1], fmaf(za.y, qz[t][k], sa[t]));
         sb[t] = fmaf(zb.x * mul[t], sc[k][t][2] + sc[k][t][3], fmaf(zb.y, qz[t][k], sb[t]));
       }
+      float la = sa[t], lb = sb[t];
       if (seen != 0xffffffffu || n0 + kBlock > lim[t]) {
-        if (!((seen >> (2 * gr)) & 1u) || n0 + gr >= lim[t]) sa[t] = -INFINITY;
-        if (!((seen >> (2 * gr + 16)) & 1u) || n0 + gr + 8 >= lim[t]) sb[t] = -INFINITY;
+        if (!((seen >> (2 * gr)) & 1u) || n0 + gr >= lim[t]) sa[t] = -INFINITY, la = INFINITY;
+        if (!((seen >> (2 * gr + 16)) & 1u) || n0 + gr + 8 >= lim[t]) sb[t] = -INFINITY, lb = INFINITY;
       }
+      low[t] = fminf(low[t], fminf(la, lb));
       raise |= fmaxf(sa[t] + lga, sb[t] + lgb) > mr[t] + kRaise;
     }
     if (__any_sync(0xffffffffu, raise)) {
@@ -1347,7 +1343,7 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 4 : 2) k_paged_few(cons
   for (int t = 0; t < NT; ++t) {
     // an infinite reference (a value scale that is infinite, on a key all rows see) leaves every weight zero, and
     // a part without weights would pass for an empty one
-    if (bad < lim[t] || mr[t] == INFINITY) lr[t] = NAN;
+    if (bad < lim[t] || mr[t] == INFINITY || low[t] == -INFINITY) lr[t] = NAN;
 #pragma unroll
     for (int o = 4; o < 32; o <<= 1) {
       lr[t] += __shfl_xor_sync(0xffffffffu, lr[t], o);
