@@ -304,8 +304,8 @@ typedef struct {
  * reads and does not change. Written: cu_rows, kv_len = ctx + new, the new block_table entries, and
  * for every row seq, pos and slot (-1 in rows that belong to no sequence).
  * report int32[4]: rows of all sequences; free pages taken in all, earlier calls' included (the next
- * call's free_used); rows without a slot because the pool or a block_table row ran out (their pages
- * read -1); pages that were lacking.
+ * call's free_used); rows without a slot because the pool or a block_table row ran out, in this call or
+ * when an earlier one should have taken their page (it reads -1); pages that were lacking.
  * No array that is written may overlap another one of the call (KVQ_ERR_INVALID): blocks read the lengths
  * while others write, so the next step's ctx_len is a copy of kv_len, and its free_used one of report[1].
  * Of pg n_seqs, n_rows, max_pages and the six arrays are used; of d batch and t_cap. n_seqs <= 16384

@@ -92,6 +92,29 @@ def test_page_map_of_two_threads_with_different_sizes():
     assert K.kvq_check(0) == K.KVQ_OK
 
 
+@gpu
+def test_page_map_reports_rows_of_a_page_that_an_earlier_call_did_not_get():
+    """The pool runs out in the middle of a prompt; the caller goes on. No later row of that page has a slot, and
+    every report says so until the rows reach a page that could be taken."""
+    d = TA.make_desc(batch=8, heads=1, tokens=0, t_cap=16, bits=2)
+    table = torch.full((2, 4), -1, dtype=torch.int32, device="cuda")
+    ctx, used = [0, 0], _i32([0])
+    free = _i32([5, 3, 6])
+    got = []
+    for new, pool in (([16, 40], free), ([1, 1], free), ([2, 6], free), ([0, 0], free), ([14, 3], _i32([5, 3, 6, 0, 7]))):
+        b = TA.make_paged(2, sum(new), 4, block_table=table)
+        rep = TA.page_map(d, b, _i32(ctx), _i32(new), pool, used).tolist()
+        assert K.kvq_check(0) == K.KVQ_OK
+        assert rep[0] == sum(new) and rep[2] == b.slot.tolist().count(-1)
+        got.append(rep[1:])
+        used = _i32([rep[1]])
+        ctx = [c + n for c, n in zip(ctx, new)]
+    # call 1: sequence 0 takes a page, sequence 1 lacks its third (positions 32 .. 39). 2: sequence 0 lacks its second,
+    # sequence 1 goes on in the lost page, position 40. 3: positions 17, 18 and 41 .. 46, all lost. 5: positions 19 .. 31
+    # of sequence 0 are lost, 32 starts a page that is there; 47 of sequence 1 is lost, 48 and 49 have one.
+    assert got == [[3, 8, 1], [3, 2, 1], [3, 8, 0], [3, 0, 0], [5, 14, 0]]
+
+
 # ---------------------------------------------------------------- steps without rows
 def test_calls_without_rows_take_null_tensors():
     """An empty tensor's address is null."""
