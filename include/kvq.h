@@ -317,8 +317,10 @@ kvq_status kvq_page_map(const kvq_desc* d, const kvq_paged* pg, const int32_t* c
 /* kvq_encode of packed rows into pages: row r of x, half [n_rows][H][head_dim] with x_stride elements
  * between rows (a multiple of 8, at least H*head_dim; 16-byte aligned), goes to record slot[r], turned
  * to position pos[r] when d->rope; the record is the one that kvq_encode gives. Sink positions (pos <
- * n_sink) are also copied to the sequence's sink row. Rows without a slot are skipped. Slots given
- * twice in one call end with either row's record. cu_rows, kv_len and block_table are not read. */
+ * n_sink) are also copied to the sequence's sink row. Rows without a slot are skipped. A slot is given
+ * to one row of a call: a record is written in pieces, so where two rows have the same slot each of its
+ * bytes is one row's or the other's, and the record need not be either's; no other record is touched.
+ * cu_rows, kv_len and block_table are not read. */
 kvq_status kvq_encode_paged(const kvq_desc* d, const void* x, int64_t x_stride, const kvq_paged* pg,
                             const kvq_tables* tb, const kvq_packed* out, kvq_stream_t stream);
 

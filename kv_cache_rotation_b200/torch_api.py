@@ -529,7 +529,8 @@ def bind_encode_paged(d: kvq_desc, x: torch.Tensor, batch: Paged, tables: Tables
 
 
 def encode_paged(d: kvq_desc, x: torch.Tensor, batch: Paged, tables: Tables, packed: Packed, stream=None) -> None:
-    """Encode the rows x fp16 [n_rows][H][D] (dense heads, any row stride) into their slots."""
+    """Encode the rows x fp16 [n_rows][H][D] (dense heads, any row stride) into their slots, each slot one
+    row's (the record of a slot given twice may be a mix of both rows')."""
     bind_encode_paged(d, x, batch, tables, packed, stream)()
 
 

@@ -239,3 +239,31 @@ def test_a_cached_record_that_is_not_finite_shows_in_every_row_that_sees_it(whic
     assert K.kvq_check(0) == K.KVQ_OK
     assert not torch.isfinite(t.out[:new[0]]).all(-1).any()
     assert torch.equal(t.out[new[0]:], clean[new[0]:])
+
+
+# ---------------------------------------------------------------- a slot of two rows
+@gpu
+@pytest.mark.parametrize("D,bits,group", [(128, 2, 128), (128, 3, 32), (64, 4, 32)])
+def test_a_slot_given_twice_holds_pieces_of_both_rows_and_nothing_else_changes(D, bits, group):
+    H, ps, n = 3, 16, 400
+    d = TA.make_desc(batch=(n + 15) // 16, heads=H, head_dim=D, tokens=0, t_cap=ps, bits=bits, group=group)
+    x = torch.randn(n, H, D, device="cuda").half()
+    slots = torch.randperm(n, device="cuda").to(torch.int32)
+    tb, pos = TA.make_tables(), torch.arange(n, dtype=torch.int32, device="cuda")
+
+    def records(rows, at):
+        pk = TA.alloc_paged(d)
+        TA.encode_paged(d, x[rows], TA.Paged(pos=pos[rows].contiguous(), slot=at), tb, pk)
+        return pk.codes.transpose(1, 2).flatten(0, 1), pk.scale_zero.transpose(1, 2).flatten(0, 1)
+    first, second = torch.arange(0, n - 100, device="cuda"), torch.arange(100, n, device="cuda")
+    own = slots[:n - 100].contiguous()
+    (c1, z1), (c2, z2) = records(first, own), records(second, own)  # rows 0 .. 299, rows 100 .. 399, on the same slots
+    both = torch.cat([first, second])
+    twice = torch.cat([own, own]).contiguous()
+    one = torch.isin(torch.arange(c1.shape[0], device="cuda"), own[50:].long())  # slots that two rows have
+    twice[n - 100:n - 50] = -1  # the second rows of the first fifty slots have none
+    c, z = records(both, twice)
+    assert K.kvq_check(0) == K.KVQ_OK
+    assert torch.equal(c[~one], c1[~one]) and torch.equal(z[~one], z1[~one])
+    assert ((c == c1) | (c == c2)).all()
+    assert ((z == z1).all(-1) | (z == z2).all(-1)).all()  # (scale, zero) of a group is one word
