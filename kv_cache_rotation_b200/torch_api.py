@@ -434,12 +434,44 @@ def alloc_paged(d: kvq_desc, sink_rows: int = 0, device="cuda", zero=True) -> Pa
     return p
 
 
-def _here(*tensors) -> None:
-    """The library launches on the current device: its tensors have to be there."""
+def _tensors(*things) -> list:
+    """The tensors of a call's arguments: of tensors, batches, caches and tables."""
+    out = []
+    for x in things:
+        out += [t for t in (vars(x).values() if isinstance(x, (Paged, Packed, Tables)) else (x,)) if t is not None]
+    return out
+
+
+def _here(*things) -> None:
+    """The library launches on the current device: all that a call reads or writes has to be there."""
     dev = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.device.index != dev:
+    for t in _tensors(*things):
+        if t.device.index != dev:
             raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{dev}")
+
+
+def _pool(d: kvq_desc, packed: Packed) -> None:
+    """The buffers of a paged cache have the descriptor's sizes: the kernels count on them."""
+    for t, name, field in ((packed.codes, "codes", KVQ_FIELD_CODES), (packed.scale_zero, "scale_zero", KVQ_FIELD_SCALE_ZERO)):
+        if t is not None:
+            _req(t, name, (t.dtype,))
+            need = kvq_packed_bytes(d, field)
+            if t.numel() * t.element_size() < need:
+                raise ValueError(f"{name}: {t.numel() * t.element_size()} bytes, the descriptor needs {need}")
+    if d.n_sink > 0 and packed.sink is not None:
+        _req(packed.sink, "sink", (torch.float16,))
+        if tuple(packed.sink.shape[1:]) != (d.heads, d.n_sink, d.head_dim):
+            raise ValueError(f"sink: shape {tuple(packed.sink.shape)}, expected (sink_rows, {d.heads}, {d.n_sink}, {d.head_dim})")
+
+
+def _row_tables(d: kvq_desc, tables: Tables) -> None:
+    """The tables that the rows of a head-variant cache read."""
+    if tables.perm is not None:
+        _req(tables.perm, "perm", (torch.int16,), (d.heads, d.head_dim))
+    if d.rope and tables.rope_cs is not None:
+        _req(tables.rope_cs, "rope_cs", (torch.float32,))
+        if tables.rope_cs.numel() != tables.rope_cs.shape[0] * d.head_dim:
+            raise ValueError(f"rope_cs: shape {tuple(tables.rope_cs.shape)}, expected (rows, {d.head_dim // 2}, 2)")
 
 
 def _meet(a: torch.Tensor, b: torch.Tensor) -> bool:
@@ -503,7 +535,7 @@ def bind_page_map(d: kvq_desc, batch: Paged, ctx_len: torch.Tensor, new_len: tor
         for other, u in [*list(writes.items())[i + 1:], *reads.items()]:
             if _meet(t, u):
                 raise ValueError(f"{name}: written while {other} is read or written, they must not overlap")
-    _here(batch.cu_rows, batch.block_table, batch.seq, ctx_len, new_len, free_pages, free_used, report)
+    _here(batch, ctx_len, new_len, free_pages, free_used, report)
     args = (ctypes.byref(d), ctypes.byref(p), ctx_len.data_ptr(), new_len.data_ptr(), free_pages.data_ptr(),
             free_pages.numel(), free_used.data_ptr(), report.data_ptr())
     return _call("kvq_page_map", args, (d, p, batch, ctx_len, new_len, free_pages, free_used, report), stream)
@@ -523,7 +555,7 @@ def page_map(d: kvq_desc, batch: Paged, ctx_len: torch.Tensor, new_len: torch.Te
 def bind_encode_paged(d: kvq_desc, x: torch.Tensor, batch: Paged, tables: Tables, packed: Packed, stream=None):
     stride = _rows(x, "x", (torch.float16,), d.heads, d.head_dim)
     p, tb, pk = batch.struct(x.shape[0], packed.sink), tables.struct(), packed.struct()
-    _here(x, batch.slot, packed.codes)
+    _pool(d, packed), _row_tables(d, tables), _here(x, batch, tables, packed)
     args = (ctypes.byref(d), x.data_ptr(), stride, ctypes.byref(p), ctypes.byref(tb), ctypes.byref(pk))
     return _call("kvq_encode_paged", args, (d, x, batch, tables, packed, p, tb, pk), stream)
 
@@ -537,7 +569,7 @@ def encode_paged(d: kvq_desc, x: torch.Tensor, batch: Paged, tables: Tables, pac
 def bind_decode_paged(d: kvq_desc, packed: Packed, batch: Paged, tables: Tables, out: torch.Tensor, stream=None):
     stride = _rows(out, "out", (torch.float16, torch.float32), d.heads, d.head_dim)
     p, tb, pk = batch.struct(out.shape[0], packed.sink), tables.struct(), packed.struct()
-    _here(out, batch.slot, packed.codes)
+    _pool(d, packed), _row_tables(d, tables), _here(out, batch, tables, packed)
     args = (ctypes.byref(d), ctypes.byref(pk), ctypes.byref(p), ctypes.byref(tb), out.data_ptr(), stride,
             1 if out.dtype == torch.float32 else 0)
     return _call("kvq_decode_paged", args, (d, packed, batch, tables, out, p, tb, pk), stream)
@@ -573,7 +605,9 @@ def bind_attend_paged(dk: kvq_desc, dv: kvq_desc, q: torch.Tensor, k_packed: Pac
         raise ValueError("sink: the two caches keep the sinks of the same sequences")
     p = batch.struct(q.shape[0], k_packed.sink)
     kp, vp, tks, tvs = k_packed.struct(), v_packed.struct(), tk.struct(), tv.struct()
-    _here(q, out, workspace, batch.block_table, k_packed.codes, v_packed.codes)
+    for d, pk, tb in ((dk, k_packed, tk), (dv, v_packed, tv)):
+        _pool(d, pk), _row_tables(d, tb)
+    _here(q, out, workspace, batch, k_packed, tk, v_packed, tv)
     args = (ctypes.byref(dk), ctypes.byref(dv), q.data_ptr(), qs, q.shape[1], ctypes.byref(kp), ctypes.byref(tks),
             ctypes.byref(vp), ctypes.byref(tvs), ctypes.byref(p), max_rows, max_kv, scale, out.data_ptr(), os,
             workspace.data_ptr(), workspace.numel())

@@ -267,3 +267,67 @@ def test_a_slot_given_twice_holds_pieces_of_both_rows_and_nothing_else_changes(D
     assert torch.equal(c[~one], c1[~one]) and torch.equal(z[~one], z1[~one])
     assert ((c == c1) | (c == c2)).all()
     assert ((z == z1).all(-1) | (z == z2).all(-1)).all()  # (scale, zero) of a group is one word
+
+
+# ---------------------------------------------------------------- what the binding checks
+class Small:
+    """A small cache and its calls, to be made wrong one argument at a time."""
+
+    def __init__(self, n_sink=4):
+        S, n, H, D, ps, pages = 2, 3, 2, 128, 16, 6
+        common = dict(batch=pages, heads=H, head_dim=D, tokens=0, t_cap=ps, bits=2, n_sink=n_sink)
+        self.dk, self.dv = TA.make_desc(rope=1, **common), TA.make_desc(rope=0, **common)
+        perm = torch.arange(D, device="cuda").flip(0).to(torch.int16).repeat(H, 1)
+        self.tk, self.tv = TA.make_tables(perm=perm, rope_cs=TA.rope_table(64, D)), TA.make_tables(perm=perm.clone())
+        self.k, self.v = TA.alloc_paged(self.dk, S), TA.alloc_paged(self.dv, S)
+        self.batch = TA.make_paged(S, n, 3, sink_slot=_i32([1, 0]))
+        self.free, self.used, self.ctx, self.new = _i32(list(range(pages))), _i32([0]), _i32([0, 0]), _i32([2, 1])
+        self.report = torch.zeros(4, dtype=torch.int32, device="cuda")
+        self.x = torch.randn(n, H, D, device="cuda").half()
+        self.q = torch.randn(n, 4, D, device="cuda").half()
+        self.out, self.back = torch.empty_like(self.q), torch.empty_like(self.x)
+        self.ws = TA.attend_paged_workspace(self.dk, self.dv, 4, self.batch, 2, 16)
+
+    def calls(self):
+        return dict(page_map=lambda: TA.bind_page_map(self.dk, self.batch, self.ctx, self.new, self.free, self.used, self.report),
+                    encode=lambda: TA.bind_encode_paged(self.dk, self.x, self.batch, self.tk, self.k),
+                    decode=lambda: TA.bind_decode_paged(self.dk, self.k, self.batch, self.tk, self.back),
+                    attend=lambda: TA.bind_attend_paged(self.dk, self.dv, self.q, self.k, self.tk, self.v, self.tv, self.batch, 2,
+                                                        16, 0.1, self.out, self.ws))
+
+
+@gpu
+@pytest.mark.parametrize("what,error", [
+    (lambda t: setattr(t.k, "codes", t.k.codes[:5]), ValueError), (lambda t: setattr(t.k, "codes", t.k.codes[:, :1]), ValueError),
+    (lambda t: setattr(t.k, "codes", t.k.codes.transpose(1, 2)), ValueError),
+    (lambda t: setattr(t.k, "scale_zero", t.k.scale_zero[:5]), ValueError),
+    (lambda t: setattr(t.k, "scale_zero", t.k.scale_zero.cpu()), ValueError),
+    (lambda t: setattr(t.k, "sink", t.k.sink[:, :1]), ValueError), (lambda t: setattr(t.k, "sink", t.k.sink[:, :, :3].contiguous()), ValueError),
+    (lambda t: setattr(t.k, "sink", t.k.sink[..., :64].contiguous()), ValueError), (lambda t: setattr(t.k, "sink", t.k.sink.float()), TypeError),
+    (lambda t: setattr(t.tk, "perm", t.tk.perm[:1].contiguous()), ValueError), (lambda t: setattr(t.tk, "perm", t.tk.perm.int()), TypeError),
+    (lambda t: setattr(t.tk, "rope_cs", t.tk.rope_cs[:, :32].contiguous()), ValueError),
+    (lambda t: setattr(t.tk, "rope_cs", t.tk.rope_cs.half()), TypeError), (lambda t: setattr(t.tk, "rope_cs", t.tk.rope_cs.cpu()), ValueError),
+], ids=["few pages", "few heads", "strides", "few scales", "host scales", "sink heads", "sink tokens", "sink width", "sink type",
+        "perm heads", "perm type", "rope width", "rope type", "host rope"])
+def test_binding_refuses_buffers_that_do_not_fit_the_descriptor(what, error):
+    t = Small()
+    what(t)
+    for name in ("encode", "decode", "attend"):
+        if name == "attend" and t.k.sink.shape != t.v.sink.shape:
+            t.v.sink = t.k.sink  # so that it is not refused for the two caches' sinks
+        with pytest.raises(error):
+            t.calls()[name]()
+
+
+@gpu
+def test_binding_looks_at_the_device_of_every_tensor(monkeypatch):
+    t = Small()
+    for name, bind in t.calls().items():
+        bind()()
+    monkeypatch.setattr(TA.torch.cuda, "current_device", lambda: 1)
+    for name, bind in t.calls().items():
+        with pytest.raises(ValueError, match="current device"):
+            bind()
+    monkeypatch.undo()
+    assert {id(x) for x in TA._tensors(t.batch, t.k, t.tk, t.q)} == {
+        id(x) for x in (*vars(t.batch).values(), t.k.codes, t.k.scale_zero, t.k.sink, t.tk.perm, t.tk.rope_cs, t.q)}
