@@ -331,3 +331,20 @@ def test_binding_looks_at_the_device_of_every_tensor(monkeypatch):
     monkeypatch.undo()
     assert {id(x) for x in TA._tensors(t.batch, t.k, t.tk, t.q)} == {
         id(x) for x in (*vars(t.batch).values(), t.k.codes, t.k.scale_zero, t.k.sink, t.tk.perm, t.tk.rope_cs, t.q)}
+
+
+@gpu
+def test_a_bound_call_is_made_on_its_device(monkeypatch):
+    """On another current device the library would launch there, on this one's addresses."""
+    t = Small()
+    calls = {name: bind() for name, bind in t.calls().items()}
+    x = torch.randn(3, 4, 128, device="cuda").half()
+    calls["prompt"] = TA.bind_attend_prompt(x[:, :2], x[:, 2:3], x[:, 3:], _i32([0, 3]), 3, 0.1, torch.empty(3, 2, 128, device="cuda").half())
+    monkeypatch.setattr(TA.torch._C, "_cuda_getDevice", lambda: 1)
+    for call in calls.values():
+        with pytest.raises(ValueError, match="cuda:1"):
+            call()
+    monkeypatch.undo()
+    for call in calls.values():
+        call()
+    assert K.kvq_check(0) == K.KVQ_OK
