@@ -515,7 +515,7 @@ def _call(name: str, args: tuple, keep: tuple, stream):
         status = fn(*args, fixed if fixed is not None else ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(dev)))
         if status != KVQ_OK:
             check(status, name)
-    call.keep = keep
+    call.keep = (keep, _tensors(*keep))  # the tensors themselves: a field of a batch or cache may get another one
     return call
 
 

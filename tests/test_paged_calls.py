@@ -348,3 +348,22 @@ def test_a_bound_call_is_made_on_its_device(monkeypatch):
     for call in calls.values():
         call()
     assert K.kvq_check(0) == K.KVQ_OK
+
+
+@gpu
+def test_a_bound_call_keeps_the_tensors_it_was_bound_to():
+    """It holds their addresses; a batch, cache or table whose field gets another tensor must not free them."""
+    import gc
+    import weakref
+    t = Small()
+    calls = {name: bind() for name, bind in t.calls().items()}
+    held = [(obj, f) for obj in (t.batch, t.k, t.v, t.tk, t.tv) for f, v in vars(obj).items() if v is not None]
+    refs = []
+    for obj, f in held:
+        refs.append(weakref.ref(getattr(obj, f)))
+        setattr(obj, f, getattr(obj, f).clone())
+    gc.collect()
+    assert all(r() is not None for r in refs)
+    del calls
+    gc.collect()
+    assert all(r() is None for r in refs)
