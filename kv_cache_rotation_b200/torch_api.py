@@ -497,6 +497,16 @@ def _rows(t: torch.Tensor, name: str, dtypes, heads=None, dim=None) -> int:
     return int(t.stride(0))
 
 
+def _new(shape, dtype, device, stream) -> torch.Tensor:
+    """A tensor that a call on `stream` writes: its memory is that stream's, so that nothing which the current
+    stream still has to do with a freed tensor's memory meets the call."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    own = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_stream(stream), device=device)
+    with torch.cuda.stream(own):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _call(name: str, args: tuple, keep: tuple, stream):
     """A zero-argument call of the entry point `name`: on `stream`, or on the stream that is current
     when it is called (so a bound call can be captured). The arguments are converted here, once: the
@@ -549,7 +559,7 @@ def page_map(d: kvq_desc, batch: Paged, ctx_len: torch.Tensor, new_len: torch.Te
     taken in all, rows without a slot, pages that were lacking. report[1:2] is the next call's free_used, and
     batch.kv_len its ctx_len: copies of them where the next call writes the same tensors."""
     if report is None:
-        report = torch.empty(4, dtype=torch.int32, device=ctx_len.device)
+        report = _new((4,), torch.int32, ctx_len.device, stream)
     bind_page_map(d, batch, ctx_len, new_len, free_pages, free_used, report, stream)()
     return report
 
@@ -646,7 +656,7 @@ def attend_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_rows: to
     """Causal attention over packed prompts: q, out [n_rows][q_heads][D], k, v [n_rows][heads][D], all
     fp16 or all bf16, cu_rows int32 [S+1]."""
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        out = _new(q.shape, q.dtype, q.device, stream)
     bind_attend_prompt(q, k, v, cu_rows, max_rows, scale, out, stream)()
     return out
 

@@ -367,3 +367,24 @@ def test_a_bound_call_keeps_the_tensors_it_was_bound_to():
     del calls
     gc.collect()
     assert all(r() is None for r in refs)
+
+
+@gpu
+@pytest.mark.parametrize("as_int", [False, True])
+def test_outputs_that_a_call_makes_belong_to_its_stream(as_int):
+    """Else the call could write memory that work of the current stream still uses."""
+    side = torch.cuda.Stream()
+    stream = side.cuda_stream if as_int else side
+
+    def owner(t):
+        for seg in torch.cuda.memory_snapshot():
+            if seg["address"] <= t.data_ptr() < seg["address"] + seg["total_size"]:
+                return seg["stream"]
+    t, x = Small(), torch.randn(3, 4, 128, device="cuda").half()
+    side.wait_stream(torch.cuda.current_stream())
+    rep = TA.page_map(t.dk, t.batch, t.ctx, t.new, t.free, t.used, stream=stream)
+    out = TA.attend_prompt(x[:, :2], x[:, 2:3], x[:, 3:], t.batch.cu_rows, 2, 0.1, stream=stream)
+    side.synchronize()
+    assert owner(rep) == owner(out) == side.cuda_stream
+    assert owner(TA.attend_prompt(x[:, :2], x[:, 2:3], x[:, 3:], t.batch.cu_rows, 2, 0.1)) == torch.cuda.current_stream().cuda_stream
+    assert rep.tolist() == [3, 2, 0, 0] and torch.isfinite(out).all()
