@@ -423,13 +423,11 @@ def make_paged(n_seqs: int, n_rows: int, max_pages: int, block_table: torch.Tens
 def alloc_paged(d: kvq_desc, sink_rows: int = 0, device="cuda", zero=True) -> Packed:
     """The buffers of a paged cache: d.batch pages of d.t_cap tokens, and the fp16 sinks of
     sink_rows sequences."""
-    n_sink, d.n_sink = d.n_sink, 0
-    try:
-        p = alloc_packed(d, device, zero)
-    finally:
-        d.n_sink = n_sink
-    if n_sink:
-        p.sink = (torch.zeros if zero else torch.empty)((sink_rows, d.heads, n_sink, d.head_dim), dtype=torch.float16,
+    bare = kvq_desc.from_buffer_copy(d)
+    bare.n_sink = 0
+    p = alloc_packed(bare, device, zero)
+    if d.n_sink:
+        p.sink = (torch.zeros if zero else torch.empty)((sink_rows, d.heads, d.n_sink, d.head_dim), dtype=torch.float16,
                                                         device=device)
     return p
 

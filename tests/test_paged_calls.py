@@ -388,3 +388,14 @@ def test_outputs_that_a_call_makes_belong_to_its_stream(as_int):
     assert owner(rep) == owner(out) == side.cuda_stream
     assert owner(TA.attend_prompt(x[:, :2], x[:, 2:3], x[:, 3:], t.batch.cu_rows, 2, 0.1)) == torch.cuda.current_stream().cuda_stream
     assert rep.tolist() == [3, 2, 0, 0] and torch.isfinite(out).all()
+
+
+def test_alloc_paged_leaves_the_descriptor_alone(monkeypatch):
+    """Another thread may be using it."""
+    d = TA.make_desc(batch=3, heads=2, tokens=0, t_cap=16, bits=2, n_sink=4)
+    seen, plain = [], TA.alloc_packed
+    monkeypatch.setattr(TA, "alloc_packed", lambda *a: (seen.append(d.n_sink), plain(*a))[1])
+    p = TA.alloc_paged(d, sink_rows=5, device="cpu")
+    assert seen == [4] and d.n_sink == 4
+    assert p.codes.shape == (3, 2, 16, 32) and p.sink.shape == (5, 2, 4, 128)
+    assert TA.alloc_paged(TA.make_desc(batch=3, heads=2, tokens=0, t_cap=16, bits=2), device="cpu").sink is None
