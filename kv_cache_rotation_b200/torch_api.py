@@ -513,6 +513,9 @@ def _call(name: str, args: tuple, keep: tuple, stream):
     types = getattr(lib, name).argtypes
     fn = lib[name]  # a handle without argtypes: the converted arguments pass as they are
     fn.restype = ctypes.c_int32
+    for t, a in zip(types, args):
+        if t is ctypes.c_int32 and not -1 << 31 <= a < 1 << 31:  # ctypes would take the low bits
+            raise ValueError(f"{name}: {a} does not fit 32 bits")
     args = tuple(t(a) if isinstance(a, (int, float)) else a for t, a in zip(types, args))
     fixed = None if stream is None else ctypes.c_void_p(_stream(stream))
     dev = torch.cuda.current_device()

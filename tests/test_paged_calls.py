@@ -399,3 +399,14 @@ def test_alloc_paged_leaves_the_descriptor_alone(monkeypatch):
     assert seen == [4] and d.n_sink == 4
     assert p.codes.shape == (3, 2, 16, 32) and p.sink.shape == (5, 2, 4, 128)
     assert TA.alloc_paged(TA.make_desc(batch=3, heads=2, tokens=0, t_cap=16, bits=2), device="cpu").sink is None
+
+
+@pytest.mark.parametrize("bad", [1 << 31, 1 << 32, -(1 << 31) - 1])
+def test_counts_that_do_not_fit_32_bits_are_refused(bad, monkeypatch):
+    """Not cut to their low bits: max_rows = 2^32 would be 0, and every row left as it was."""
+    monkeypatch.setattr(TA.torch.cuda, "current_device", lambda: 0)
+    good = (4096, 1024, 4096, 256, 4096, 256, 0, 0, 8, 2, 128, 0, 4096, 0, 0.1, 4096, 1024)
+    TA._call("kvq_attend_prompt", good, (), 0)()  # no row: nothing is launched
+    for i in (6, 7, 8, 9, 10, 11, 13):
+        with pytest.raises(ValueError, match="32 bits"):
+            TA._call("kvq_attend_prompt", good[:i] + (bad,) + good[i + 1:], (), 0)
