@@ -532,6 +532,7 @@ def _call(name: str, args: tuple, keep: tuple, stream):
 
 def bind_page_map(d: kvq_desc, batch: Paged, ctx_len: torch.Tensor, new_len: torch.Tensor, free_pages: torch.Tensor,
                   free_used: torch.Tensor, report: torch.Tensor, stream=None):
+    d = kvq_desc.from_buffer_copy(d)  # here and below: the call is made with what was checked
     p = batch.struct()
     for name in ("cu_rows", "kv_len", "block_table", "seq", "pos", "slot"):
         if getattr(batch, name) is None:
@@ -566,6 +567,7 @@ def page_map(d: kvq_desc, batch: Paged, ctx_len: torch.Tensor, new_len: torch.Te
 
 
 def bind_encode_paged(d: kvq_desc, x: torch.Tensor, batch: Paged, tables: Tables, packed: Packed, stream=None):
+    d = kvq_desc.from_buffer_copy(d)
     stride = _rows(x, "x", (torch.float16,), d.heads, d.head_dim)
     p, tb, pk = batch.struct(x.shape[0], packed.sink), tables.struct(), packed.struct()
     _pool(d, packed), _row_tables(d, tables), _here(x, batch, tables, packed)
@@ -580,6 +582,7 @@ def encode_paged(d: kvq_desc, x: torch.Tensor, batch: Paged, tables: Tables, pac
 
 
 def bind_decode_paged(d: kvq_desc, packed: Packed, batch: Paged, tables: Tables, out: torch.Tensor, stream=None):
+    d = kvq_desc.from_buffer_copy(d)
     stride = _rows(out, "out", (torch.float16, torch.float32), d.heads, d.head_dim)
     p, tb, pk = batch.struct(out.shape[0], packed.sink), tables.struct(), packed.struct()
     _pool(d, packed), _row_tables(d, tables), _here(out, batch, tables, packed)
@@ -608,6 +611,7 @@ def attend_paged_workspace(dk: kvq_desc, dv: kvq_desc, q_heads: int, batch: Page
 def bind_attend_paged(dk: kvq_desc, dv: kvq_desc, q: torch.Tensor, k_packed: Packed, tk: Tables, v_packed: Packed,
                       tv: Tables, batch: Paged, max_rows: int, max_kv: int, scale: float, out: torch.Tensor,
                       workspace: torch.Tensor, stream=None):
+    dk, dv = kvq_desc.from_buffer_copy(dk), kvq_desc.from_buffer_copy(dv)
     qs = _rows(q, "q", (torch.float16,), None, dk.head_dim)
     os = _rows(out, "out", (torch.float16,), q.shape[1], dk.head_dim)
     if out.shape[0] != q.shape[0]:

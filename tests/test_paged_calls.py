@@ -410,3 +410,19 @@ def test_counts_that_do_not_fit_32_bits_are_refused(bad, monkeypatch):
     for i in (6, 7, 8, 9, 10, 11, 13):
         with pytest.raises(ValueError, match="32 bits"):
             TA._call("kvq_attend_prompt", good[:i] + (bad,) + good[i + 1:], (), 0)
+
+
+@gpu
+def test_a_bound_call_is_made_with_the_descriptor_it_was_bound_with():
+    """Buffers were checked against that one; a later change of it must not reach the kernels."""
+    t = Small()
+    calls = {name: bind() for name, bind in t.calls().items()}
+    for call in calls.values():
+        call()
+    want = [x.clone() for x in (t.batch.block_table, t.k.codes, t.back, t.out)]
+    # values that the library refuses, should they reach it
+    t.dk.batch = t.dv.batch = 0
+    for call in calls.values():
+        call()
+    assert K.kvq_check(0) == K.KVQ_OK
+    assert all(torch.equal(a, b) for a, b in zip(want, (t.batch.block_table, t.k.codes, t.back, t.out)))
