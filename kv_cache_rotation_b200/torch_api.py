@@ -436,30 +436,34 @@ def _tensors(*things) -> list:
     """The tensors of a call's arguments: of tensors, batches, caches and tables."""
     out = []
     for x in things:
-        out += [t for t in (vars(x).values() if isinstance(x, (Paged, Packed, Tables)) else (x,)) if t is not None]
+        if isinstance(x, torch.Tensor):
+            out.append(x)
+        elif isinstance(x, (Paged, Packed, Tables)):
+            out += [t for t in vars(x).values() if t is not None]
     return out
 
 
-def _here(*things) -> None:
+def _here(tensors) -> None:
     """The library launches on the current device: all that a call reads or writes has to be there."""
     dev = torch.cuda.current_device()
-    for t in _tensors(*things):
-        if t.device.index != dev:
+    for t in tensors:
+        if t.get_device() != dev:
             raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{dev}")
 
 
 def _pool(d: kvq_desc, packed: Packed) -> None:
     """The buffers of a paged cache have the descriptor's sizes: the kernels count on them."""
-    for t, name, field in ((packed.codes, "codes", KVQ_FIELD_CODES), (packed.scale_zero, "scale_zero", KVQ_FIELD_SCALE_ZERO)):
+    H, D, n_sink = d.heads, d.head_dim, d.n_sink
+    records = d.batch * H * d.t_cap
+    for t, name, each in ((packed.codes, "codes", D * d.bits // 8), (packed.scale_zero, "scale_zero", D // max(d.group, 1) * 4)):
         if t is not None:
             _req(t, name, (t.dtype,))
-            need = kvq_packed_bytes(d, field)
-            if t.numel() * t.element_size() < need:
-                raise ValueError(f"{name}: {t.numel() * t.element_size()} bytes, the descriptor needs {need}")
-    if d.n_sink > 0 and packed.sink is not None:
+            if t.nbytes < records * each:
+                raise ValueError(f"{name}: {t.nbytes} bytes, the descriptor needs {records * each}")
+    if n_sink > 0 and packed.sink is not None:
         _req(packed.sink, "sink", (torch.float16,))
-        if tuple(packed.sink.shape[1:]) != (d.heads, d.n_sink, d.head_dim):
-            raise ValueError(f"sink: shape {tuple(packed.sink.shape)}, expected (sink_rows, {d.heads}, {d.n_sink}, {d.head_dim})")
+        if tuple(packed.sink.shape[1:]) != (H, n_sink, D):
+            raise ValueError(f"sink: shape {tuple(packed.sink.shape)}, expected (sink_rows, {H}, {n_sink}, {D})")
 
 
 def _row_tables(d: kvq_desc, tables: Tables) -> None:
@@ -472,10 +476,44 @@ def _row_tables(d: kvq_desc, tables: Tables) -> None:
             raise ValueError(f"rope_cs: shape {tuple(tables.rope_cs.shape)}, expected (rows, {d.head_dim // 2}, 2)")
 
 
+def _span(t: torch.Tensor):
+    """First byte of a tensor, and the byte behind its last."""
+    a, n = t.data_ptr(), t.numel()
+    if n and not t.is_contiguous():
+        n = 1 + sum((d - 1) * s for d, s in zip(t.shape, t.stride()))
+    return a, a + n * t.element_size()
+
+
 def _meet(a: torch.Tensor, b: torch.Tensor) -> bool:
-    """Whether two contiguous tensors share memory."""
-    return (a.numel() > 0 and b.numel() > 0 and a.data_ptr() < b.data_ptr() + b.numel() * b.element_size()
-            and b.data_ptr() < a.data_ptr() + a.numel() * a.element_size())
+    """Whether two tensors, dense ones or packed rows with a stride, share memory: slices of one projection do not,
+    though they lie between each other (with different strides whatever lies so counts as shared)."""
+    (a0, a1), (b0, b1) = _span(a), _span(b)
+    if a0 == a1 or b0 == b1 or a0 >= b1 or b0 >= a1:
+        return False
+    fars = {t.stride(0) * t.element_size() for t in (a, b) if t.shape[0] > 1}
+    if len(fars) != 1:
+        return True
+    far, off = fars.pop(), b0 - a0  # bytes between rows; where b's rows begin behind a's
+    one, two = (t.nbytes // t.shape[0] for t in (a, b))
+    return off % far < one or off % far + two > far
+
+
+def _apart(writes: dict, reads) -> None:
+    """No tensor that a call writes shares memory with one that it reads, or with another one that it writes."""
+    outs = {n: t for n, t in writes.items() if t is not None}
+    spans = sorted([(*_span(t), True) for t in outs.values()] + [(*_span(t), False) for t in reads])
+    end = written = 0  # of all spans so far, and of the written ones
+    for a, e, w in spans:
+        if a < e and (a < written or (w and a < end)):
+            break
+        end, written = max(end, e), max(written, e) if w else written
+    else:
+        return  # nearly always; what follows is for spans that lie between each other
+    names = list(outs)
+    for i, name in enumerate(names):
+        for u in (*reads, *(outs[o] for o in names[i + 1:])):
+            if _meet(outs[name], u):
+                raise ValueError(f"{name}: an output must not overlap what the call reads or writes beside it")
 
 
 def _rows(t: torch.Tensor, name: str, dtypes, heads=None, dim=None) -> int:
@@ -505,7 +543,7 @@ def _new(shape, dtype, device, stream) -> torch.Tensor:
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _call(name: str, args: tuple, keep: tuple, stream):
+def _call(name: str, args: tuple, keep: tuple, stream, why=None):
     """A zero-argument call of the entry point `name`: on `stream`, or on the stream that is current
     when it is called (so a bound call can be captured). The arguments are converted here, once: the
     call costs the library's own time and about 3 us. It is refused on another current device."""
@@ -525,6 +563,8 @@ def _call(name: str, args: tuple, keep: tuple, stream):
             raise ValueError(f"{name}: bound on cuda:{dev}, called on cuda:{torch.cuda.current_device()}")
         status = fn(*args, fixed if fixed is not None else ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(dev)))
         if status != KVQ_OK:
+            if why is not None:
+                why()
             check(status, name)
     call.keep = (keep, _tensors(*keep))  # the tensors themselves: a field of a batch or cache may get another one
     return call
@@ -542,17 +582,19 @@ def bind_page_map(d: kvq_desc, batch: Paged, ctx_len: torch.Tensor, new_len: tor
     _req(free_pages, "free_pages", (torch.int32,), (free_pages.numel(),))
     _req(free_used, "free_used", (torch.int32,), (1,))
     _req(report, "report", (torch.int32,), (4,))
-    reads = dict(ctx_len=ctx_len, new_len=new_len, free_pages=free_pages, free_used=free_used)
-    writes = {n: getattr(batch, n) for n in ("cu_rows", "kv_len", "block_table", "seq", "pos", "slot")}
-    writes["report"] = report
-    for i, (name, t) in enumerate(writes.items()):
-        for other, u in [*list(writes.items())[i + 1:], *reads.items()]:
-            if _meet(t, u):
-                raise ValueError(f"{name}: written while {other} is read or written, they must not overlap")
-    _here(batch, ctx_len, new_len, free_pages, free_used, report)
+    _here(_tensors(batch, ctx_len, new_len, free_pages, free_used, report))
     args = (ctypes.byref(d), ctypes.byref(p), ctx_len.data_ptr(), new_len.data_ptr(), free_pages.data_ptr(),
             free_pages.numel(), free_used.data_ptr(), report.data_ptr())
-    return _call("kvq_page_map", args, (d, p, batch, ctx_len, new_len, free_pages, free_used, report), stream)
+
+    def why():  # the library refuses arrays that overlap, this says which
+        reads = dict(ctx_len=ctx_len, new_len=new_len, free_pages=free_pages, free_used=free_used)
+        writes = {n: getattr(batch, n) for n in ("cu_rows", "kv_len", "block_table", "seq", "pos", "slot")}
+        writes["report"] = report
+        for i, (name, t) in enumerate(writes.items()):
+            for other, u in [*list(writes.items())[i + 1:], *reads.items()]:
+                if _meet(t, u):
+                    raise ValueError(f"{name}: written while {other} is read or written, they must not overlap")
+    return _call("kvq_page_map", args, (d, p, batch, ctx_len, new_len, free_pages, free_used, report), stream, why)
 
 
 def page_map(d: kvq_desc, batch: Paged, ctx_len: torch.Tensor, new_len: torch.Tensor, free_pages: torch.Tensor,
@@ -570,7 +612,10 @@ def bind_encode_paged(d: kvq_desc, x: torch.Tensor, batch: Paged, tables: Tables
     d = kvq_desc.from_buffer_copy(d)
     stride = _rows(x, "x", (torch.float16,), d.heads, d.head_dim)
     p, tb, pk = batch.struct(x.shape[0], packed.sink), tables.struct(), packed.struct()
-    _pool(d, packed), _row_tables(d, tables), _here(x, batch, tables, packed)
+    _pool(d, packed), _row_tables(d, tables)
+    reads = _tensors(x, batch, tables)
+    _here(reads + _tensors(packed))
+    _apart(dict(codes=packed.codes, scale_zero=packed.scale_zero, sink=packed.sink if d.n_sink else None), reads)
     args = (ctypes.byref(d), x.data_ptr(), stride, ctypes.byref(p), ctypes.byref(tb), ctypes.byref(pk))
     return _call("kvq_encode_paged", args, (d, x, batch, tables, packed, p, tb, pk), stream)
 
@@ -585,7 +630,10 @@ def bind_decode_paged(d: kvq_desc, packed: Packed, batch: Paged, tables: Tables,
     d = kvq_desc.from_buffer_copy(d)
     stride = _rows(out, "out", (torch.float16, torch.float32), d.heads, d.head_dim)
     p, tb, pk = batch.struct(out.shape[0], packed.sink), tables.struct(), packed.struct()
-    _pool(d, packed), _row_tables(d, tables), _here(out, batch, tables, packed)
+    _pool(d, packed), _row_tables(d, tables)
+    reads = _tensors(batch, tables, packed)
+    _here(reads + [out])
+    _apart(dict(out=out), reads)
     args = (ctypes.byref(d), ctypes.byref(pk), ctypes.byref(p), ctypes.byref(tb), out.data_ptr(), stride,
             1 if out.dtype == torch.float32 else 0)
     return _call("kvq_decode_paged", args, (d, packed, batch, tables, out, p, tb, pk), stream)
@@ -624,7 +672,9 @@ def bind_attend_paged(dk: kvq_desc, dv: kvq_desc, q: torch.Tensor, k_packed: Pac
     kp, vp, tks, tvs = k_packed.struct(), v_packed.struct(), tk.struct(), tv.struct()
     for d, pk, tb in ((dk, k_packed, tk), (dv, v_packed, tv)):
         _pool(d, pk), _row_tables(d, tb)
-    _here(q, out, workspace, batch, k_packed, tk, v_packed, tv)
+    reads = _tensors(q, batch, k_packed, tk, v_packed, tv)
+    _here(reads + [out, workspace])
+    _apart(dict(out=out, workspace=workspace), reads)
     args = (ctypes.byref(dk), ctypes.byref(dv), q.data_ptr(), qs, q.shape[1], ctypes.byref(kp), ctypes.byref(tks),
             ctypes.byref(vp), ctypes.byref(tvs), ctypes.byref(p), max_rows, max_kv, scale, out.data_ptr(), os,
             workspace.data_ptr(), workspace.numel())
@@ -650,7 +700,8 @@ def bind_attend_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_row
     _req(cu_rows, "cu_rows", (torch.int32,))
     if cu_rows.dim() != 1 or cu_rows.numel() < 1:
         raise ValueError(f"cu_rows: shape {tuple(cu_rows.shape)}, expected (sequences + 1,)")
-    _here(q, k, v, out, cu_rows)
+    _here((q, k, v, out, cu_rows))
+    _apart(dict(out=out), (q, k, v, cu_rows))
     args = (q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, cu_rows.numel() - 1, n, hq, k.shape[1], dim,
             KVQ_BF16 if q.dtype == torch.bfloat16 else KVQ_F16, cu_rows.data_ptr(), max_rows, scale, out.data_ptr(), os)
     return _call("kvq_attend_prompt", args, (q, k, v, cu_rows, out), stream)

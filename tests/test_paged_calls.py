@@ -426,3 +426,59 @@ def test_a_bound_call_is_made_with_the_descriptor_it_was_bound_with():
         call()
     assert K.kvq_check(0) == K.KVQ_OK
     assert all(torch.equal(a, b) for a, b in zip(want, (t.batch.block_table, t.k.codes, t.back, t.out)))
+
+
+def test_shared_memory_of_rows_with_strides():
+    """Against the addresses of the elements themselves."""
+    buf = torch.zeros(4000, dtype=torch.int16)
+
+    def at(t):
+        return set((torch.arange(4000).as_strided(t.shape, t.stride(), t.storage_offset()) if t.numel() else torch.empty(0)).flatten().tolist())
+    r = random.Random(3)
+    both = 0
+    for _ in range(4000):
+        far = r.choice([40, 64])
+        t = [buf.as_strided((r.randint(0, 5), r.choice([1, 2, 3]), 8), (far, 8, 1), r.randint(0, 90)) for _ in range(2)]
+        meets = bool(at(t[0]) & at(t[1]))
+        for a, b in (t, t[::-1]):
+            if t[0].stride(0) == t[1].stride(0):
+                assert TA._meet(a, b) == meets
+            else:  # with different strides whatever lies between each other counts
+                assert TA._meet(a, b) or not meets
+        both += meets
+    assert 500 < both < 3500
+    x = buf[:3000].view(50, 6, 10)
+    assert not TA._meet(x[:, :2], x[:, 2:4]) and TA._meet(x[:, :3], x[:, 2:4]) and TA._meet(x, x) and not TA._meet(x[:20], x[20:])
+    flat = buf[:16].view(torch.int32)
+    assert TA._meet(flat[:4], flat[3:]) and not TA._meet(flat[:4], flat[4:])
+
+
+@gpu
+@pytest.mark.parametrize("name,what", [
+    ("encode", lambda t: setattr(t, "x", t.k.codes.view(-1)[:1536].view(torch.float16).view(3, 2, 128))),
+    ("encode", lambda t: setattr(t.k, "sink", t.x[:2].unsqueeze(0).repeat(2, 1, 2, 1).contiguous()) or setattr(t, "x", t.k.sink.view(-1)[:768].view(3, 2, 128))),
+    ("decode", lambda t: setattr(t, "back", t.k.codes.view(-1)[:1536].view(torch.float16).view(3, 2, 128))),
+    ("decode", lambda t: setattr(t, "back", t.tk.rope_cs.view(-1)[:768].view(3, 2, 128))),
+    ("attend", lambda t: setattr(t, "out", t.q)),
+    ("attend", lambda t: setattr(t, "out", t.ws[:3072].view(torch.float16).view(3, 4, 128))),
+    ("attend", lambda t: setattr(t, "ws", t.v.codes.view(-1))),
+], ids=["rows in the codes", "rows in the sinks", "codes", "table", "queries", "workspace", "values"])
+def test_outputs_that_overlap_are_refused(name, what):
+    t = Small()
+    what(t)
+    with pytest.raises(ValueError, match="overlap"):
+        t.calls()[name]()
+
+
+@gpu
+def test_prompt_outputs_beside_the_inputs_and_over_them():
+    x = torch.randn(40, 4 + 2 * 2 + 4, 128, device="cuda").half()  # q, k, v and room for the output in one buffer
+    q, k, v, room = x[:, :4], x[:, 4:6], x[:, 6:8], x[:, 8:]
+    cu = _i32([0, 40])
+    want = TA.attend_prompt(q.clone(), k.clone(), v.clone(), cu, 40, 0.1)
+    for over in (q, x[:, 2:6], x[:, 4:8], x[:, 7:11]):
+        with pytest.raises(ValueError, match="overlap"):
+            TA.attend_prompt(q, k, v, cu, 40, 0.1, over)
+    TA.attend_prompt(q, k, v, cu, 40, 0.1, room)
+    assert K.kvq_check(0) == K.KVQ_OK
+    assert torch.equal(room, want)
