@@ -246,3 +246,67 @@ def test_a_serving_run_within_its_roundings(bits, group, n_sink, perm):
     assert max(shares) <= 1.0
     held = table[table >= 0].tolist()
     assert len(set(held)) == len(held) == sum(-(-c // ps) for c in ctx)
+
+
+# ---------------------------------------------------------------- records and queries of other sizes
+def _flat(sz, r):
+    sz[..., 0] = 0.0
+
+
+def _some_flat(sz, r):
+    sz[..., 0] *= (r < 0.5)
+
+
+def _some_zero(sz, r):
+    sz *= (r < 0.5)[..., None]
+
+
+def _wide(sz, r):
+    sz *= (2.0 ** torch.floor(r * 16 - 8))[..., None]
+
+
+KINDS = dict(flat=_flat, some_flat=_some_flat, some_zero=_some_zero, wide=_wide, peaked=None, tiny_queries=None, large_queries=None)
+
+
+@gpu
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("new,bits,group,few", [([1, 2], 2, 128, True), ([2, 2], 4, 32, True), ([17, 1], 3, 64, False), ([70, 3], 2, 64, False)],
+                         ids=["few", "few_g32", "one_slot", "two_slots"])
+def test_records_and_queries_of_all_sizes(new, bits, group, few, kind):
+    """Groups without a range (a token of zeros, of equal values), ranges from 2^-8 to 2^7 of the usual, scores far apart,
+    queries near fp16's ends: in keys, values and both."""
+    from test_paged import Attend
+    for which in ((0,), (1,), (0, 1)) if KINDS[kind] else ((),):
+        t = Attend([900, 60], new, 4, 1, 128, bits, group, 1, True, 2, "fwht_head", 16, 1, seed=len(kind))
+        g = torch.Generator(device="cuda").manual_seed(4)
+        for i in which:
+            sz = t.packs[i].scale_zero.view(torch.float16)
+            x = sz.float()
+            KINDS[kind](x, torch.rand(x.shape[:-1], device="cuda", generator=g))
+            sz.copy_(torch.where(torch.isnan(sz), sz, x.half()))
+        if not which:
+            t.q.mul_({"peaked": 20.0, "tiny_queries": 2.0 ** -14, "large_queries": 2000.0}[kind])
+            t.scale *= {"peaked": 1.0, "tiny_queries": 2.0 ** 14, "large_queries": 0.001}[kind]
+        t.call()()
+        assert K.kvq_check(0) == K.KVQ_OK
+        _check(t, few)
+
+
+@gpu
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("new,Hq,bits,n_sink", [([1, 3], 2, 2, 4), ([4, 1], 4, 4, 0), ([20, 9], 8, 3, 1), ([200, 70], 8, 2, 4)],
+                         ids=["few", "few_two", "one_slot", "two_slots"])
+def test_a_query_row_that_is_not_finite_touches_no_other(new, Hq, bits, n_sink, bad):
+    from test_paged import Attend
+    t = Attend([300, 40], new, Hq, 2, 128, bits, 128, 1, False, n_sink, "fwht_head", 16)
+    t.call()()
+    clean = t.out.clone()
+    row, head = new[0] - 1, Hq - 1
+    t.q[row, head, 5] = bad
+    t.out.fill_(7.0)
+    t.call()()
+    assert K.kvq_check(0) == K.KVQ_OK
+    assert not torch.isfinite(t.out[row, head]).any()
+    clean[row, head] = 0.0
+    t.out[row, head] = 0.0
+    assert torch.equal(t.out, clean)

@@ -132,3 +132,18 @@ def test_two_slots_captured_and_two_at_once():
     assert K.kvq_check(0) == K.KVQ_OK
     _check(y, lens, Hq, H, outs[0], 0.1, 600)
     _check(xs[1].cpu(), lens, Hq, H, outs[1], 0.1, 600)
+
+
+@gpu
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("lens,Hq,H", [([70, 300], 8, 2), ([70, 300, 700], 64, 16)], ids=["one_slot", "two_slots"])
+def test_a_query_row_that_is_not_finite_touches_no_other(lens, Hq, H, bad):
+    x, cu = _inputs(lens, Hq, H, 128, "f16", 0, seed=5)
+    assert _two_slots(lens, Hq, H) == (H == 16)
+    clean = _run(x, cu, Hq, H, max(lens), 0.1)
+    x[200, Hq - 1, 5] = bad
+    got = _run(x, cu, Hq, H, max(lens), 0.1)
+    assert K.kvq_check(0) == K.KVQ_OK
+    assert not torch.isfinite(got[200, Hq - 1]).any()
+    got[200, Hq - 1] = clean[200, Hq - 1] = 0.0
+    assert torch.equal(got, clean)
