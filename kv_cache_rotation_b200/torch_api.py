@@ -469,7 +469,9 @@ def _pool(d: kvq_desc, packed: Packed) -> None:
 def _row_tables(d: kvq_desc, tables: Tables) -> None:
     """The tables that the rows of a head-variant cache read."""
     if tables.perm is not None:
-        _req(tables.perm, "perm", (torch.int16,), (d.heads, d.head_dim))
+        _req(tables.perm, "perm", (torch.int16,))
+        if tables.perm.numel() != d.heads * d.head_dim:
+            raise ValueError(f"perm: shape {tuple(tables.perm.shape)}, expected ({d.heads}, {d.head_dim})")
     if d.rope and tables.rope_cs is not None:
         _req(tables.rope_cs, "rope_cs", (torch.float32,))
         if tables.rope_cs.numel() != tables.rope_cs.shape[0] * d.head_dim:
@@ -546,7 +548,7 @@ def _new(shape, dtype, device, stream) -> torch.Tensor:
 def _call(name: str, args: tuple, keep: tuple, stream, why=None):
     """A zero-argument call of the entry point `name`: on `stream`, or on the stream that is current
     when it is called (so a bound call can be captured). The arguments are converted here, once: the
-    call costs the library's own time and about 3 us. It is refused on another current device."""
+    call costs the library's own time and about 2 us. It is refused on another current device."""
     from . import KVQ_OK, lib
     types = getattr(lib, name).argtypes
     fn = lib[name]  # a handle without argtypes: the converted arguments pass as they are
@@ -557,9 +559,10 @@ def _call(name: str, args: tuple, keep: tuple, stream, why=None):
     args = tuple(t(a) if isinstance(a, (int, float)) else a for t, a in zip(types, args))
     fixed = None if stream is None else ctypes.c_void_p(_stream(stream))
     dev = torch.cuda.current_device()
+    others = torch.cuda.device_count() > 1  # else no other device can be current, and asking costs 1 us
 
     def call():
-        if torch.cuda.current_device() != dev:
+        if others and torch.cuda.current_device() != dev:
             raise ValueError(f"{name}: bound on cuda:{dev}, called on cuda:{torch.cuda.current_device()}")
         status = fn(*args, fixed if fixed is not None else ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(dev)))
         if status != KVQ_OK:
@@ -710,7 +713,8 @@ def bind_attend_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_row
 def attend_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_rows: torch.Tensor, max_rows: int,
                   scale: float, out: torch.Tensor = None, stream=None) -> torch.Tensor:
     """Causal attention over packed prompts: q, out [n_rows][q_heads][D], k, v [n_rows][heads][D], all
-    fp16 or all bf16, cu_rows int32 [S+1]."""
+    fp16 or all bf16, cu_rows int32 [S+1]. Rows that no sequence has, or beyond max_rows, are not written:
+    where out is not given they hold whatever its memory held."""
     if out is None:
         out = _new(q.shape, q.dtype, q.device, stream)
     bind_attend_prompt(q, k, v, cu_rows, max_rows, scale, out, stream)()

@@ -337,14 +337,15 @@ def test_binding_looks_at_the_device_of_every_tensor(monkeypatch):
 def test_a_bound_call_is_made_on_its_device(monkeypatch):
     """On another current device the library would launch there, on this one's addresses."""
     t = Small()
+    monkeypatch.setattr(TA.torch.cuda, "device_count", lambda: 2)
     calls = {name: bind() for name, bind in t.calls().items()}
     x = torch.randn(3, 4, 128, device="cuda").half()
     calls["prompt"] = TA.bind_attend_prompt(x[:, :2], x[:, 2:3], x[:, 3:], _i32([0, 3]), 3, 0.1, torch.empty(3, 2, 128, device="cuda").half())
-    monkeypatch.setattr(TA.torch._C, "_cuda_getDevice", lambda: 1)
-    for call in calls.values():
-        with pytest.raises(ValueError, match="cuda:1"):
-            call()
-    monkeypatch.undo()
+    with monkeypatch.context() as m:
+        m.setattr(TA.torch.cuda, "current_device", lambda: 1)
+        for call in calls.values():
+            with pytest.raises(ValueError, match="cuda:1"):
+                call()
     for call in calls.values():
         call()
     assert K.kvq_check(0) == K.KVQ_OK
@@ -405,6 +406,7 @@ def test_alloc_paged_leaves_the_descriptor_alone(monkeypatch):
 def test_counts_that_do_not_fit_32_bits_are_refused(bad, monkeypatch):
     """Not cut to their low bits: max_rows = 2^32 would be 0, and every row left as it was."""
     monkeypatch.setattr(TA.torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(TA.torch.cuda, "device_count", lambda: 1)
     good = (4096, 1024, 4096, 256, 4096, 256, 0, 0, 8, 2, 128, 0, 4096, 0, 0.1, 4096, 1024)
     TA._call("kvq_attend_prompt", good, (), 0)()  # no row: nothing is launched
     for i in (6, 7, 8, 9, 10, 11, 13):
@@ -482,3 +484,17 @@ def test_prompt_outputs_beside_the_inputs_and_over_them():
     TA.attend_prompt(q, k, v, cu, 40, 0.1, room)
     assert K.kvq_check(0) == K.KVQ_OK
     assert torch.equal(room, want)
+
+
+@gpu
+def test_a_permutation_of_any_shape_is_taken():
+    """The library reads H * head_dim numbers; a flat tensor of them is as good."""
+    t = Small()
+    flat = {name: bind for name, bind in t.calls().items()}
+    t.tk.perm, t.tv.perm = t.tk.perm.view(-1), t.tv.perm.view(1, -1)
+    for bind in flat.values():
+        bind()()
+    assert K.kvq_check(0) == K.KVQ_OK
+    t.tk.perm = t.tk.perm[:-1].contiguous()
+    with pytest.raises(ValueError, match="perm"):
+        t.calls()["encode"]()
