@@ -17,11 +17,13 @@
 // k_paged_merge: a warp, or eight, per row and query head joins them with the sinks
 // and turns the result back.
 //
-// Measured, 32 / 8 heads of 128: 512 rows on 16384 keys of 4 bits 212 us = 660 TFLOP/s
-// (41 % of the products' rate): a slot's softmax of a tile, 2400 to 2800 clocks beside
+// Measured, 32 / 8 heads of 128: 512 rows on 16384 keys of 4 bits 212 to 216 us = 650 TFLOP/s
+// (40 % of the products' rate): a slot's softmax of a tile, 2400 to 2800 clocks beside
 // the record warps, and its products take turns, 4370 clocks for two slots' tile; a CTA's
-// set-up, first tile and epilogue are 20000 more. Tensor pipe 39 %, exponentials 40 %.
-// Twelve sequences of 1 to 131 rows on up to 8000 keys of 3 bits 176 us.
+// set-up, first tile and epilogue are 20000 more. Tensor pipe 40 %, exponentials 40 %.
+// Twelve sequences of 1 to 131 rows on up to 8000 keys of 3 bits 175 us. The registers are
+// full: the two-slot forms spill 156 to 226 bytes a thread, the one-slot forms 68 to 84, and
+// part of it is in the loop (local loads and stores are 1.3 % of the chunk's instructions).
 #include <math.h>
 
 #include "kvq_flash.cuh"
@@ -877,9 +879,10 @@ __global__ void __launch_bounds__(256) k_paged_merge(const PagedArgs a) {
 // A weight p S is at most 2^15: the reference m follows s + log2 S (S >= 2^-30)
 // and is raised when that exceeds it by 2^8; p = 2^(s - m + 7).
 //
-// Measured, 2 bits, one group, 32 / 8 heads: 64 sequences of up to 8191 keys 85 us (159
-// MB, 1.9 TB/s), four of 32768 keys 45 us. 271 instructions per 16 keys and warp, about
-// 80 of them masks and shifts of codes: ALU pipe 52 %, issue 55 %, DRAM 26 %.
+// Measured, 2 bits, one group, 32 / 8 heads: 64 sequences of up to 8191 keys 87 us (159
+// MB, 1.8 TB/s), four of 32768 keys 45 us, each with its merge. 253 warp instructions per
+// 16 keys, 16 of them products, and 3500 a CTA: ALU pipe 52 to 55 %, issue 56 to 57 %,
+// DRAM 25 %; 118 registers, nothing spilled.
 constexpr int kFewWarps = 4;
 constexpr int kFewThreads = 32 * kFewWarps;
 constexpr int kBlock = 16;
@@ -1381,6 +1384,9 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 4 : 2) k_paged_few(cons
   }
 }
 
+// The SMs that work is cut for. A constant, not the device's count: the workspace's size follows from the cut, and its
+// query is a pure function that needs no device. On any other count every result is the same, only the cut is less apt.
+constexpr int kPlanSms = 148;
 // How a call's work is cut: row tiles, and stretches of keys per tile.
 struct Plan {
   bool shared, few;
@@ -1392,6 +1398,11 @@ Plan make_plan(const kvq_desc& d, int q_heads, int n_seqs, int n_rows, int max_r
   Plan p{};
   const int g = q_heads / heads;
   p.T = 128 / g;
+  // The few-rows kernel where it has a form: its code maps are for 128 channels and codes that do not straddle words,
+  // and more than eight rows would need a third column tile (the second takes 190 to 229 registers). At 2 bits 64
+  // ragged sequences took 278 us through tiles and take 87 here. What it has no form for takes tiles of 128 rows for
+  // its few: the same batch 323 us at 3 bits, 241 at 64 channels, 323 with 16 rows a head. The rule looks at the whole
+  // call: one sequence with more rows sends all of them through tiles.
   p.few = d.head_dim == 128 && d.bits != 3 && static_cast<long long>(max_rows) * g <= 8 &&
           static_cast<long long>(d.heads) * d.t_cap * 64 < (1ll << 31);  // a page's codes in 32 bits
   p.shared = max_rows > p.T;
@@ -1399,13 +1410,14 @@ Plan make_plan(const kvq_desc& d, int q_heads, int n_seqs, int n_rows, int max_r
   const long long by_rows = n_rows / tt + n_seqs, by_max = n_seqs * ((max_rows + tt - 1) / tt);
   p.tiles = p.few ? n_seqs : by_rows < by_max ? by_rows : by_max;
   // Few rows: eight CTAs an SM (four at a time), so that ragged sequences even out; 64 sequences of up
-  // to 8192 keys took 107 us with four an SM and 85 with eight, four of 32768 keys 43 and 45. Tiles, each
+  // to 8192 keys took 107 us with four an SM and 85 with eight, four of 32768 keys 43 and 45 (before the check of
+  // infinite keys, which costs the first 1 us). Tiles, each
   // CTA with about 20000 clocks besides its keys: one CTA an SM at most where all sequences have the most
   // rows (512 rows on 16384 keys took 212 us so, 269, 227 and 234 with three, four and six stretches),
   // about two where they are ragged (twelve sequences of 1 to 131 rows on up to 8000 keys took 201 us with
   // one stretch, 178 with two or three, 193 with six).
   const long long all = p.tiles * heads, keys = max_kv > 0 ? max_kv : 1;
-  long long n = all <= 0 ? 1 : p.few ? 8 * 148 / all : by_rows < by_max ? (2 * 148 + all - 1) / all : 148 / all;
+  long long n = all <= 0 ? 1 : p.few ? 8 * kPlanSms / all : by_rows < by_max ? (2 * kPlanSms + all - 1) / all : kPlanSms / all;
   const long long most = (keys + 511) / 512;  // of at least 512 keys
   n = n < 1 ? 1 : n > most ? most : n;
   if (n > 256) n = 256;
@@ -1435,7 +1447,9 @@ kvq_status run_few(const PagedArgs& a, long long grid, cudaStream_t st) {
   return launch_status();
 }
 
-// Eight warps a row where there are more parts than a warp should read one after the other.
+// Eight warps a row where there are more parts than a warp should read one after the other. With one warp and with
+// eight, whole calls: 8 parts 13.7 and 14.4 us (16 sequences of 1000 keys, a token each), 32.3 and 49.1 (100 rows on
+// 4000 keys); 12 parts 17.9 and 15.4, 16 parts 21.7 and 17.3 (1500 and 2000 keys).
 constexpr int kNarrow = 8;
 template <int D, int BITS, bool TILE>
 kvq_status run_merge(const PagedArgs& a, cudaStream_t st) {

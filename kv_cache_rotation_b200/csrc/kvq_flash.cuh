@@ -255,8 +255,9 @@ struct RowItem {
 
 // Tile `idx` (of `tile` rows): under a causal mask a sequence's last tiles take longest and come first.
 // Up to 32 sequences: all sequences' tiles by their place in the sequence, from the last on. More: from
-// the last sequence's last tile backwards. One warp; item->len is 0 when there is no such tile. Offsets
-// are cut to [0, n_rows] and to ascending order.
+// the last sequence's last tile backwards, a dependent step per 32 sequences (31 for the first of 1000
+// sequences, in every CTA) and without an order by length. One warp; item->len is 0 when there is no such
+// tile. Offsets are cut to [0, n_rows] and to ascending order.
 __device__ __forceinline__ void find_item(const int32_t* cu_rows, int n_seqs, int n_rows, int max_rows, int tile,
                                           int idx, int lane, RowItem* item) {
   if (lane == 0) item->len = 0;

@@ -201,9 +201,10 @@ __global__ void __launch_bounds__(kMapThreads) k_page_map(const MapArgs a) {
 // (every lane computes fma(own, +-1, partner): exactly a + b below and a - b
 // above), D/2 inside the pairs. Rows go head-fastest, so the heads of a token
 // share its (cos, sin) row in L1. With the permutation the L1 data pipe is the
-// bound (67 to 80 % busy: gather, shuffles, (cos, sin) rows; issue 55 to 65 %):
+// bound (75 to 87 % busy: gather, shuffles, (cos, sin) rows; issue 54 to 64 %):
 // K and V of 30119 rows of 8 heads in and out, 4 bits, groups of 64, half-split
-// RoPE, take 224 us for 347 MB (1.55 TB/s, 24 % of a copy's rate).
+// RoPE, take 224 us for 318 MB (1.42 TB/s, 22 % of a copy's rate), the table of
+// 2940 positions counted once.
 constexpr int kRowThreads = 256;
 
 struct RowArgs {

@@ -15,10 +15,11 @@
 // Warps: 0-3 and 4-7 softmax of slots 0 and 1; 8 loads; 9 issues the products;
 // 10 and 11 clear what the mask hides in V (see below).
 //
-// Measured: 16384 tokens of 8 / 2 heads of 128, bf16, 525 us = 1047 TFLOP/s, at the
-// power limit (1.37 GHz; tensor pipe and exponentials 51 % each, in turn). Nine
-// prompts, 6500 tokens, 32 / 8 heads, 118 us: set-up and epilogue of a CTA (about 4500
-// clocks) and a short grid's tail. One prompt of 77 tokens 8.5 us: a launch and one chain.
+// Measured: 16384 tokens of 8 / 2 heads of 128, bf16, 531 us = 1036 TFLOP/s call after call, at the
+// power limit (1.37 GHz); tensor pipe and exponentials 57 % of a launch's cycles each, in turn. Nine
+// prompts, 6500 tokens, 32 / 8 heads, 118 us: set-up and epilogue of a CTA (about 4500 clocks) and a
+// short grid's tail. One prompt of 77 tokens 8.8 us: a launch and one chain. The registers are full (20
+// bytes a thread spilled with two slots, 48 to 56 with one).
 //
 // Masked keys get weight 0, but 0 * inf is not 0, so V must be finite wherever
 // a weight is masked: only the last tiles of a CTA (from the diagonal on) hold
@@ -152,7 +153,7 @@ __global__ void __launch_bounds__(Split<SLOTS>::kThreads, 3 - SLOTS)
       const bool dirty = *reinterpret_cast<volatile int*>(&m->dirty) != 0;
       // Two slots (many CTAs): out over the slot's query rows, which nothing reads any more, so that a store writes
       // 128 bytes of each of four rows and not 16 of 32 (nine prompts 118 us against 122). One slot (a call that does
-      // not fill the SMs): straight out, which is sooner done (77 tokens 8.5 us against 8.9).
+      // not fill the SMs): straight out, which is sooner done (77 tokens 8.5 us against 8.9 when this was chosen).
       uint8_t* const rows = gbase + t * C::kHead;
       T* const own = static_cast<T*>(a.p.out) + (static_cast<int64_t>(row0) + tok) * a.p.out_stride + (h * a.g + r % a.g) * D;
 #pragma unroll
