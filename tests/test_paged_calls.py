@@ -498,3 +498,75 @@ def test_a_permutation_of_any_shape_is_taken():
     t.tk.perm = t.tk.perm[:-1].contiguous()
     with pytest.raises(ValueError, match="perm"):
         t.calls()["encode"]()
+
+
+# ---------------------------------------------------------------- offsets beyond 32 bits
+@gpu
+@pytest.mark.parametrize("bits,new", [(4, [1, 2]), (2, [1, 1]), (3, [40, 3]), (4, [60, 1])], ids=["few", "few_2", "one_slot", "two_slots"])
+def test_pages_whose_records_lie_beyond_4_gb(bits, new):
+    """The same records in a small pool and at the far end of a large one: the same bytes out."""
+    H, D, ps, Hq, S = 8, 128, 64, 32, 2
+    far = ((1 << 32) + (1 << 28)) // (H * ps * D * bits // 8)  # pages
+    n, ctx = sum(new), [100, 30]
+    g = torch.Generator(device="cuda").manual_seed(bits)
+    x = torch.randn(n + sum(ctx), Hq + 2 * H, D, device="cuda", generator=g).half()
+    got = []
+    for pages in (16, far):
+        common = dict(batch=pages, heads=H, head_dim=D, tokens=0, t_cap=ps, bits=bits, n_sink=1)
+        dk, dv = TA.make_desc(rope=1, **common), TA.make_desc(rope=0, **common)
+        tk, tv = TA.make_tables(rope_cs=TA.rope_table(256, D)), TA.make_tables()
+        kc, vc = TA.alloc_paged(dk, S, zero=False), TA.alloc_paged(dv, S, zero=False)
+        free, used = _i32([pages - 1 - i for i in range(8)]), _i32([0])
+        table, have, at = torch.full((S, 4), -1, dtype=torch.int32, device="cuda"), [0, 0], 0
+        for step in (ctx, new):
+            m = sum(step)
+            b = TA.make_paged(S, m, 4, block_table=table)
+            rep = TA.page_map(dk, b, _i32(have), _i32(step), free, used)
+            rows = x[at:at + m]
+            TA.encode_paged(dk, rows[:, Hq:Hq + H], b, tk, kc)
+            TA.encode_paged(dv, rows[:, Hq + H:], b, tv, vc)
+            at, used, have = at + m, rep[1:2].clone(), [h + s for h, s in zip(have, step)]
+        assert int(b.slot.min()) * H * D * bits // 8 > (1 << 32) or pages == 16
+        back = torch.empty(m, H, D, dtype=torch.float16, device="cuda")
+        TA.decode_paged(dv, vc, b, tv, back)
+        out = torch.empty(m, Hq, D, dtype=torch.float16, device="cuda")
+        ws = TA.attend_paged_workspace(dk, dv, Hq, b, max(new), 256)
+        TA.attend_paged(dk, dv, rows[:, :Hq], kc, tk, vc, tv, b, max(new), 256, D ** -0.5, out, ws)
+        assert K.kvq_check(0) == K.KVQ_OK
+        got.append((back, out))
+    assert torch.isfinite(got[0][1]).all() and got[0][1].abs().max() > 0.1
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+
+
+@gpu
+def test_rows_whose_strides_pass_32_bits():
+    """Row strides of 2^23 elements: row 300 begins beyond 4 GB."""
+    n, Hq, H, D, far = 300, 4, 2, 128, 1 << 23
+    buf = torch.empty(n * far, dtype=torch.float16, device="cuda")
+
+    def rows(at, heads):
+        return buf.as_strided((n, heads, D), (far, D, 1), at)
+    q, k, v, out, back = rows(0, Hq), rows(1024, H), rows(2048, H), rows(4096, Hq), rows(8192, H)
+    g = torch.Generator(device="cuda").manual_seed(2)
+    for t in (q, k, v):
+        t.copy_(torch.randn(t.shape, device="cuda", generator=g))
+    out.fill_(7.0), back.fill_(7.0)
+    cu = _i32([0, 20, n])
+    TA.attend_prompt(q, k, v, cu, n, 0.1, out)
+    assert torch.equal(out, TA.attend_prompt(q.contiguous(), k.contiguous(), v.contiguous(), cu, n, 0.1))
+    common = dict(batch=24, heads=H, head_dim=D, tokens=0, t_cap=16, bits=4)
+    dk, dv = TA.make_desc(rope=1, **common), TA.make_desc(rope=0, **common)
+    tk, tv = TA.make_tables(rope_cs=TA.rope_table(300, D)), TA.make_tables()
+    b = TA.make_paged(2, n, 18)
+    TA.page_map(dk, b, _i32([0, 0]), _i32([20, n - 20]), _i32(list(range(24))), _i32([0]))
+    got = []
+    for near in (False, True):
+        kc, vc = TA.alloc_paged(dk), TA.alloc_paged(dv)
+        x = [t.contiguous() if near else t for t in (q, k, v)]
+        o, r = (torch.empty(n, Hq, D, dtype=torch.float16, device="cuda"), torch.empty(n, H, D, dtype=torch.float16, device="cuda")) if near else (out, back)
+        TA.encode_paged(dk, x[1], b, tk, kc), TA.encode_paged(dv, x[2], b, tv, vc)
+        TA.decode_paged(dk, kc, b, tk, r)
+        TA.attend_paged(dk, dv, x[0], kc, tk, vc, tv, b, 280, 280, 0.1, o, TA.attend_paged_workspace(dk, dv, Hq, b, 280, 280))
+        got.append([t.clone() for t in (kc.codes, vc.codes, r, o)])
+    assert K.kvq_check(0) == K.KVQ_OK
+    assert all(torch.equal(a, c) for a, c in zip(*got))

@@ -310,3 +310,37 @@ def test_a_query_row_that_is_not_finite_touches_no_other(new, Hq, bits, n_sink, 
     clean[row, head] = 0.0
     t.out[row, head] = 0.0
     assert torch.equal(t.out, clean)
+
+
+# ---------------------------------------------------------------- shapes between the listed ones
+@gpu
+@pytest.mark.parametrize("Hq,H,new,ps,bits,group", [
+    (3, 1, [1, 2, 1], 100, 2, 128), (9, 3, [2, 0, 1], 16, 4, 64), (10, 2, [1, 1, 0], 5, 2, 32), (7, 1, [1, 1, 1], 33, 4, 128),
+    (6, 6, [8, 3, 5], 64, 2, 64), (5, 5, [7, 0, 1], 1, 4, 32), (12, 2, [1, 1, 1], 512, 2, 128)])
+def test_few_rows_of_odd_groups_and_pages(Hq, H, new, ps, bits, group):
+    from test_paged import Attend
+    t = Attend([333, 0, 1100], new, Hq, H, 128, bits, group, 1, True, 3, "fwht_head", ps, 1, seed=Hq)
+    t.call()()
+    assert K.kvq_check(0) == K.KVQ_OK
+    _check(t, True)
+
+
+@gpu
+def test_few_rows_of_many_sequences():
+    from test_paged import Attend
+    ctx = [(71 * i) % 400 for i in range(300)]
+    t = Attend(ctx, [(i % 7 != 3) * 1 for i in range(300)], 4, 1, 128, 2, 128, 1, False, 2, "fwht_head", 16, 3)
+    t.call()()
+    assert K.kvq_check(0) == K.KVQ_OK
+    _check(t, True)
+
+
+@gpu
+@pytest.mark.parametrize("Hq,H,new,ps", [(3, 1, [50, 9], 100), (10, 2, [13, 40], 33), (5, 1, [26, 1], 7), (11, 1, [12, 30], 512)])
+def test_tiles_of_odd_groups_and_pages(Hq, H, new, ps):
+    from test_paged import Attend
+    for bits, group, D in ((4, 64, 128), (3, 32, 64)):
+        t = Attend([333, 1100], new, Hq, H, D, bits, group, 2, True, 3, "fwht_head", ps, 1, seed=Hq)
+        t.call()()
+        assert K.kvq_check(0) == K.KVQ_OK
+        _check(t, False)
