@@ -462,7 +462,7 @@ def test_shared_memory_of_rows_with_strides():
     ("decode", lambda t: setattr(t, "back", t.k.codes.view(-1)[:1536].view(torch.float16).view(3, 2, 128))),
     ("decode", lambda t: setattr(t, "back", t.tk.rope_cs.view(-1)[:768].view(3, 2, 128))),
     ("attend", lambda t: setattr(t, "out", t.q)),
-    ("attend", lambda t: setattr(t, "out", t.ws[:3072].view(torch.float16).view(3, 4, 128))),
+    ("attend", lambda t: setattr(t, "out", t.ws[:t.q.nbytes].view(torch.float16).view(3, 4, 128))),
     ("attend", lambda t: setattr(t, "ws", t.v.codes.view(-1))),
 ], ids=["rows in the codes", "rows in the sinks", "codes", "table", "queries", "workspace", "values"])
 def test_outputs_that_overlap_are_refused(name, what):
